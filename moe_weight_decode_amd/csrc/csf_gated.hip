@@ -408,8 +408,8 @@ __device__ __forceinline__ Tile find_tile(const uint32_t *prefix, const int32_t 
         ++e;
         mts = expert_tiles(expert_start, e, S, s0, m);
     }
-    const uint32_t j = tile - before, blocks = (m + 15u) / 16u, b0 = blocks * j / mts, b1 = blocks * (j + 1u) / mts;
-    return {e, s0 + 16u * b0, min(16u * (b1 - b0), m - 16u * b0), (b1 - b0 + 1u) / 2u};
+    const TileBlocks b = tile_blocks(m, tile - before, mts);
+    return {e, s0 + 16u * b.first, min(16u * b.count, m - 16u * b.first), (b.count + 1u) / 2u};
 }
 
 // Tiles left are handed out by counters in `queue`, one for each XCD's

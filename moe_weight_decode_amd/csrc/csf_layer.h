@@ -116,6 +116,20 @@ struct GatedBackwardArgs {
 
 constexpr uint32_t kGatedQueueBytes = 64;  // one counter per XCD
 
+// A tile's share of the blocks of 16 slots of an expert with m of them: its
+// first block and how many.
+struct TileBlocks {
+    uint32_t first, count;
+};
+
+// Tile j of the `tiles` that an expert's slots are spread over: all have q
+// blocks, the first r of them one more.  No product passes the blocks' number,
+// as blocks * j would (32 bits hold it up to three million slots only).
+__host__ __device__ inline TileBlocks tile_blocks(uint32_t m, uint32_t j, uint32_t tiles) {
+    const uint32_t blocks = (m + 15u) / 16u, q = blocks / tiles, r = blocks - q * tiles;
+    return {q * j + (j < r ? j : r), q + (j < r ? 1u : 0u)};
+}
+
 // Whether a call has enough slots per expert for the tile kernel (which reads
 // dense scales), and whether its activations lie within that one's reach.
 bool gated_by_tiles(uint32_t E, uint32_t S);
