@@ -898,7 +898,10 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_dx_kernel(GatedBac
         const Tile at = find_tile(s_prefix, a.expert_start, a.E, a.S, mt);
         const uint32_t e = at.e, t0 = at.t0, count = at.count;
         const float alpha = a.alpha[e];
-        const rsrc_t rd = make_rsrc(a.dgu + (uint64_t)t0 * N, count * N * 2u);  // slots past the tile's read 0
+        // Slots past the tile's and rows past 2F read 0: the range's own end is past it at every offset.  A constant would
+        // not be, since 128 slots of up to 2^24 - 2 rows reach 2^32 - 512 bytes.
+        const uint32_t past = count * N * 2u;
+        const rsrc_t rd = make_rsrc(a.dgu + (uint64_t)t0 * N, past);
         const rsrc_t rw = make_rsrc(a.w + (uint64_t)e * N * (K / 2u), N * (K / 2u));
         const uint8_t *scales = a.dense + (uint64_t)e * N * C;
         const bool some = k0 + kDxWave * wave < K;  // the wave has columns
@@ -924,7 +927,7 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_dx_kernel(GatedBac
 #pragma unroll
                     for (uint32_t i = 0; i < 4; ++i) {
                         const uint32_t r = (wave * 4u + i) * 8u + lane / 8u, c = (lane ^ (r >> 1)) & 7u;
-                        const uint32_t off = nb + 8u * c < N ? r * N * 2u + 16u * c : kOutside;
+                        const uint32_t off = nb + 8u * c < N ? r * N * 2u + 16u * c : past;
                         __builtin_amdgcn_raw_ptr_buffer_load_lds(
                             rd, (__attribute__((address_space(3))) void *)(buffer(which) + (wave * 4u + i) * 1024u), 16, (int)off, (int)(from * 2u), 0, 0);
                     }
@@ -932,7 +935,7 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_dx_kernel(GatedBac
                     for (uint32_t i = 0; i < 16; ++i) {
                         const uint32_t r = (wave * 16u + i) * 2u + lane / 32u, c = ((lane % 32u) / 4u ^ (r >> 1)) & 7u;
                         const uint32_t n = 8u * c + 2u * (lane & 3u);
-                        const uint32_t off = nb + n < N ? r * N * 2u + n * 2u : kOutside;
+                        const uint32_t off = nb + n < N ? r * N * 2u + n * 2u : past;
                         __builtin_amdgcn_raw_ptr_buffer_load_lds(
                             rd, (__attribute__((address_space(3))) void *)(buffer(which) + (wave * 16u + i) * 256u), 4, (int)off, (int)(from * 2u), 0, 0);
                     }

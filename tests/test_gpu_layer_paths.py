@@ -1,13 +1,14 @@
 """Sizes and uses of the layer operators that reach their further code paths:
 large counts, other streams, graphs of bound calls, kernels chosen for many
 tokens.  Bounds and helpers are those of test_gpu_layer."""
+import ctypes
 
 import numpy as np
 import pytest
 import torch
 
 import workloads
-from test_gpu_layer import Gated, normal
+from test_gpu_layer import U, Gated, f64, near, normal
 
 csf = pytest.importorskip("moe_weight_decode_amd")
 
@@ -36,3 +37,39 @@ def test_millions_of_slots_of_one_expert(dev, S):
     assert torch.equal(hs, h[at]) and torch.equal(gus, gu[at])
     dxs, dgus = csf.moe_gated_backward(c.stack, c.dense(), c.tw, dh[at], gus, c.ta, es)
     assert torch.equal(dxs, dx[at]) and torch.equal(dgus, dgu[at])
+
+
+def test_gated_backward_of_millions_of_rows(dev):
+    # 128 slots of 2F = 9,000,032 rows: 2.3 GB of dgu in a tile, past 31-bit offsets.  The last step of 64 rows is half
+    # full; what its other half reads must be 0 for every slot, whatever stands in another slot's rows.
+    S, N, K = 128, 9_000_032, 32
+    F = N // 2
+    g = torch.Generator(device=dev)
+    g.manual_seed(4)
+    gu = torch.randn(S, N, generator=g, device=dev, dtype=torch.bfloat16)
+    dh = torch.randn(S, F, generator=g, device=dev, dtype=torch.bfloat16)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device=dev, dtype=torch.uint8)
+    dense = torch.full((N,), 127, dtype=torch.uint8, device=dev)
+    es, alpha = torch.tensor([0, S], dtype=torch.int32, device=dev), torch.full((1,), 0.25, device=dev)
+    d = csf.csf_stack()
+    d.format, d.num_experts, d.rows, d.cols = csf.MXFP4, 1, N, 1
+
+    def backward():
+        dx, dgu = torch.empty(S, K, dtype=torch.bfloat16, device=dev), torch.empty(S, N, dtype=torch.bfloat16, device=dev)
+        assert csf.library().csf_moe_gated_backward(
+            ctypes.byref(d), dense.data_ptr(), codes.data_ptr(), dh.data_ptr(), gu.data_ptr(), S, alpha.data_ptr(), es.data_ptr(),
+            dx.data_ptr(), dgu.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        return dx, dgu
+
+    dx, dgu = backward()
+    table = torch.tensor((0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0), device=dev)
+    w = table[torch.stack((codes & 15, codes >> 4), 2).flatten(1).int()].double()
+    for s in (0, 127):
+        v = dgu[s].double()
+        want, mag = 0.25 * (v @ w), 0.25 * (v.abs() @ w.abs())
+        # a running sum is rounded once per 32 rows, and a product's 32 terms add their own roundings
+        near(dx[s], f64(want), 2.0 ** -8 * np.abs(f64(want)) + (N // 32 + 40) * U * f64(mag), "dx")
+    del w, dgu
+    gu[120] = float("nan")
+    bad, _ = backward()
+    assert bad[120].isnan().all() and torch.equal(bad[:120], dx[:120]) and torch.equal(bad[121:], dx[121:])
