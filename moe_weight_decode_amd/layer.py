@@ -6,7 +6,9 @@ its tensors (device, type, size, contiguity), allocates its outputs and its
 workspace, enqueues on ``stream`` (default: the current one) and returns
 without synchronising.  A ``stream`` other than the current one first waits for
 the current stream's queued work, since the outputs' memory is allocated there;
-work on another stream that uses the results must wait for ``stream``.
+work on another stream that uses the results must wait for ``stream``.  Inputs
+may be dropped as soon as the call returns; one that is written again must wait
+for ``stream`` too.
 
 ``bound(function, *args, **kwargs)`` checks and marshals a call once: the
 returned object enqueues the same call on the same buffers each time it is
@@ -119,12 +121,22 @@ def _ptr(t):
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
+def _tensors(values):
+    """Every tensor among a call's values, a stack's own included."""
+    for v in values:
+        if isinstance(v, CompressedStack):
+            yield from _tensors((v.bases, v.offsets, v.exceptions, v.prefix, v.tile_index))
+        elif isinstance(v, torch.Tensor):
+            yield v
+
+
 def _call(name, args, result, dev, inputs, fresh, side) -> Bound:
     _lib()  # fills _functions
     if side is not None:
-        for t in fresh:  # allocated on the current stream, written on `stream`
-            if t is not None:
-                t.record_stream(side)
+        # Used on `stream`, but allocated on others, where the memory of what the caller drops (the inputs, as soon as
+        # the call returns) would be handed out again at once: kept until `stream` is done with it.
+        for t in _tensors((*inputs, *fresh)):
+            t.record_stream(side)
     return Bound(name, args, result, (inputs, fresh))
 
 

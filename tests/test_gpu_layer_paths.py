@@ -73,3 +73,50 @@ def test_gated_backward_of_millions_of_rows(dev):
     gu[120] = float("nan")
     bad, _ = backward()
     assert bad[120].isnan().all() and torch.equal(bad[:120], dx[:120]) and torch.equal(bad[121:], dx[121:])
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def test_inputs_dropped_after_a_call_on_another_stream(dev):
+    """Inputs freed when the call returns, `stream` still busy: what the current
+    stream allocates and writes next must not be their memory."""
+    rng = np.random.default_rng(17)
+    T, D, E, k = 600, 512, 16, 2
+    S = T * k
+    c = Gated(4, 24, 64, [9, 0, 33, 20], workloads.NVFP4, seed=18, T=31)
+    w = 1.0 + normal(rng, D, scale=0.1)
+    x, y, logits = normal(rng, T, D, dtype=torch.bfloat16), normal(rng, S, D), normal(rng, T, E)
+    r, n = csf.route(logits, k), csf.rms_norm(x, w, x)
+    dh = normal(rng, len(c.rows), c.F, dtype=torch.bfloat16)
+    gu, dense, dg = c.forward(save=True)[1], c.dense(), normal(rng, T, k)
+    calls = [
+        (lambda v, **kw: csf.rms_norm(*v, **kw), (x, w, x)),
+        (lambda v, **kw: csf.rms_norm(v[0], v[1], v[2], slots=v[3], gates=v[4], **kw), (y, w, x, r.slots, r.gates)),
+        (lambda v, **kw: csf.rms_norm_backward(*v, **kw), (x, n.sum, w, n.rstd, x)),
+        (lambda v, **kw: csf.route(*v, k, **kw), (logits,)),
+        (lambda v, **kw: csf.combine_backward(*v, **kw), (x, y, r.slots, r.gates)),
+        (lambda v, **kw: csf.route_backward(*v, **kw), (dg, logits, r.experts, r.gates)),
+        (lambda v, **kw: csf.moe_gated(c.stack, *v, **kw), (c.tw, c.x, c.ta, c.te, c.tr)),
+        (lambda v, **kw: csf.moe_gated_backward(c.stack, *v, **kw), (dense, c.tw, dh, gu, c.ta, c.te)),
+    ]
+    side = torch.cuda.Stream()
+    busy = torch.empty(64 << 20, dtype=torch.float32, device=dev)
+
+    def outputs(got):
+        got = (got,) if isinstance(got, torch.Tensor) else got
+        return [t for t in got if t is not None]
+
+    for call, inputs in calls:
+        want = outputs(call(inputs))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for i in range(20):  # a few milliseconds
+                busy.fill_(float(i))
+        copies = [t.clone() for t in inputs]
+        sizes = [(t.shape, t.dtype) for t in copies]
+        got = outputs(call(copies, stream=side))
+        del copies
+        junk = [torch.full(shape, 0x55, dtype=dtype, device=dev) for shape, dtype in sizes]
+        side.synchronize()
+        assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
