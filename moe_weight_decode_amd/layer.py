@@ -5,15 +5,17 @@ Argument marshalling only, as the rest of the binding.  Every function checks
 its tensors (device, type, size, contiguity), allocates its outputs and its
 workspace, enqueues on ``stream`` (default: the current one) and returns
 without synchronising.  A ``stream`` other than the current one first waits for
-the current stream's queued work, since the outputs' memory is allocated there;
-work on another stream that uses the results must wait for ``stream``.  Inputs
-may be dropped as soon as the call returns; one that is written again must wait
-for ``stream`` too.
+the current stream's queued work, since the inputs may come from it and the
+outputs' memory is allocated there; work on another stream that uses the
+results must wait for ``stream``.  Inputs may be dropped as soon as the call
+returns; one that is written again must wait for ``stream`` too.
 
 ``bound(function, *args, **kwargs)`` checks and marshals a call once: the
 returned object enqueues the same call on the same buffers each time it is
-called and returns the same outputs, for decode loops whose buffers stay and
-for graph capture.
+called and returns the same outputs, for decode loops whose buffers stay.  It
+goes to the stream that is current when it is called (or to ``stream``, with
+the wait above at every call), so it can be bound first and captured in a graph
+later; the graph uses its buffers, which live as long as the bound call.
 """
 from __future__ import annotations
 
@@ -73,18 +75,37 @@ _functions = {}  # the library's functions by name
 
 
 class Bound:
-    """One checked and marshalled call; calling it enqueues it again."""
-    __slots__ = ("_fn", "_args", "_result", "_name", "_keep")
+    """One checked and marshalled call; calling it enqueues it again, on the
+    stream given when it was bound or else on the current one."""
+    __slots__ = ("_fn", "_args", "_result", "_name", "_keep", "_dev", "_stream", "_known")
 
-    def __init__(self, name: str, args: tuple, result, keep):
+    def __init__(self, name: str, args: tuple, result, keep, dev, stream):
         self._fn, self._name = _functions[name], name
         self._args, self._result, self._keep = args, result, keep
+        self._dev, self._stream = dev, stream
+        self._known = {_current(dev.index)}  # streams that the tensors' memory waits for when it is freed
 
     def __call__(self):
-        status = self._fn(*self._args)
+        if self._stream is None:
+            handle = _current(self._dev.index)
+        else:
+            handle = _enter(self._stream, self._dev)
+        if handle not in self._known:
+            self._record(handle)
+        status = self._fn(*self._args, handle)
         if status != 0:
             raise CsfError(status, self._name)
         return self._result
+
+    def _record(self, handle):
+        """Used on a stream that they were not allocated on, the tensors' memory
+        would be handed out again as soon as they are dropped (the inputs of a
+        plain call when it returns): it is kept until that stream is done."""
+        stream = _stream_of(handle, self._dev)
+        inputs, fresh = self._keep
+        for t in _tensors((*inputs, *fresh)):
+            t.record_stream(stream)
+        self._known.add(handle)
 
 
 # the handle of the current stream, without a Stream object where torch offers that
@@ -104,17 +125,17 @@ def _device(where: str, t, name: str):
     return t.device
 
 
+def _stream_of(handle, dev):
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
 def _enter(stream, dev):
-    """The stream's handle; a stream other than the current one, which then waits for that."""
-    if stream is None:
-        return _current(dev.index), None
+    """The stream's handle; one other than the current stream first waits for that."""
     current = torch.cuda.current_stream(dev)
     handle = _stream_handle(stream, dev)
-    if handle == current.cuda_stream:
-        return handle, None
-    side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
-    side.wait_stream(current)
-    return handle, side
+    if handle != current.cuda_stream:
+        _stream_of(handle, dev).wait_stream(current)
+    return handle
 
 
 def _ptr(t):
@@ -130,14 +151,9 @@ def _tensors(values):
             yield v
 
 
-def _call(name, args, result, dev, inputs, fresh, side) -> Bound:
+def _call(name, args, result, dev, inputs, fresh, stream) -> Bound:
     _lib()  # fills _functions
-    if side is not None:
-        # Used on `stream`, but allocated on others, where the memory of what the caller drops (the inputs, as soon as
-        # the call returns) would be handed out again at once: kept until `stream` is done with it.
-        for t in _tensors((*inputs, *fresh)):
-            t.record_stream(side)
-    return Bound(name, args, result, (inputs, fresh))
+    return Bound(name, args, result, (inputs, fresh), dev, stream)
 
 
 def _rms_norm(x, weight, residual=None, slots=None, gates=None, eps=1e-6, mxfp8=False, stream=None) -> Bound:
@@ -162,15 +178,14 @@ def _rms_norm(x, weight, residual=None, slots=None, gates=None, eps=1e-6, mxfp8=
     if residual is not None:
         _need(where, "residual", residual, tuple(DTYPES) if slots is not None else (x.dtype,), dev, T * D)
     _need(where, "weight", weight, (torch.float32,), dev, D)
-    handle, side = _enter(stream, dev)
     total = x if residual is None else torch.empty(T, D, dtype=dtype, device=dev)
     out = torch.empty(T, D, dtype=torch.uint8 if mxfp8 else dtype, device=dev)
     scales = torch.empty(T, (D + 31) // 32, dtype=torch.uint8, device=dev) if mxfp8 else None
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
     args = (DTYPES[dtype], _ptr(x), _ptr(residual), weight.data_ptr(), T, D, _ptr(slots), _ptr(gates), k,
-            x.shape[0], eps, None if residual is None else _ptr(total), _ptr(out), _ptr(scales), _ptr(rstd), handle)
+            x.shape[0], eps, None if residual is None else _ptr(total), _ptr(out), _ptr(scales), _ptr(rstd))
     fresh = (out, scales, rstd, None if residual is None else total)
-    return _call("csf_rms_norm", args, Normed(out, total, rstd, scales), dev, (x, weight, residual, slots, gates), fresh, side)
+    return _call("csf_rms_norm", args, Normed(out, total, rstd, scales), dev, (x, weight, residual, slots, gates), fresh, stream)
 
 
 def _rms_norm_backward(dy, sum, weight, rstd, dsum=None, stream=None) -> Bound:
@@ -183,14 +198,13 @@ def _rms_norm_backward(dy, sum, weight, rstd, dsum=None, stream=None) -> Bound:
     _need(where, "rstd", rstd, (torch.float32,), dev, T)
     if dsum is not None:
         _need(where, "dsum", dsum, (dy.dtype,), dev, T * D)
-    handle, side = _enter(stream, dev)
     dx = torch.empty_like(dy)
     dweight = torch.empty(D, dtype=torch.float32, device=dev)
     need = _lib().csf_rms_norm_backward_workspace(T, D)
     workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     args = (DTYPES[dy.dtype], _ptr(dy), _ptr(sum), weight.data_ptr(), _ptr(rstd), _ptr(dsum), T, D, _ptr(dx),
-            dweight.data_ptr(), workspace.data_ptr(), need, handle)
-    return _call("csf_rms_norm_backward", args, (dx, dweight), dev, (dy, sum, weight, rstd, dsum), (dx, dweight, workspace), side)
+            dweight.data_ptr(), workspace.data_ptr(), need)
+    return _call("csf_rms_norm_backward", args, (dx, dweight), dev, (dy, sum, weight, rstd, dsum), (dx, dweight, workspace), stream)
 
 
 def _route(logits, topk, renorm=True, stream=None) -> Bound:
@@ -200,15 +214,14 @@ def _route(logits, topk, renorm=True, stream=None) -> Bound:
     T, E = logits.shape
     if not 1 <= topk <= min(E, 64) or E > MAX_EXPERTS:
         raise ValueError(f"{where}: topk must be 1 to min(E, 64), E at most {MAX_EXPERTS}")
-    handle, side = _enter(stream, dev)
     need = _lib().csf_route_workspace(T, E)
     workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     r = Routing(torch.empty(T, topk, dtype=torch.int32, device=dev), torch.empty(T, topk, dtype=torch.float32, device=dev),
                 torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(T * topk, dtype=torch.int32, device=dev),
                 torch.empty(T, topk, dtype=torch.int32, device=dev))
     args = (DTYPES[logits.dtype], _ptr(logits), T, E, topk, int(bool(renorm)), _ptr(r.experts), _ptr(r.gates),
-            r.expert_start.data_ptr(), _ptr(r.rows), _ptr(r.slots), _ptr(workspace), need, handle)
-    return _call("csf_route", args, r, dev, (logits,), (*r, workspace), side)
+            r.expert_start.data_ptr(), _ptr(r.rows), _ptr(r.slots), _ptr(workspace), need)
+    return _call("csf_route", args, r, dev, (logits,), (*r, workspace), stream)
 
 
 def _combine_backward(dout, y, slots, gates, stream=None) -> Bound:
@@ -222,11 +235,10 @@ def _combine_backward(dout, y, slots, gates, stream=None) -> Bound:
     if y.shape[1] != D or slots.shape[0] != T or k < 1:
         raise ValueError(f"{where}: y must be [S, {D}] and slots [{T}, k]")
     _need(where, "gates", gates, (torch.float32,), dev, T * k)
-    handle, side = _enter(stream, dev)
     dy = torch.empty(y.shape, dtype=dout.dtype, device=dev)
     dgates = torch.empty(T, k, dtype=torch.float32, device=dev)
-    args = (DTYPES[dout.dtype], _ptr(dout), _ptr(y), _ptr(slots), _ptr(gates), T, k, D, y.shape[0], _ptr(dy), _ptr(dgates), handle)
-    return _call("csf_combine_backward", args, (dy, dgates), dev, (dout, y, slots, gates), (dy, dgates), side)
+    args = (DTYPES[dout.dtype], _ptr(dout), _ptr(y), _ptr(slots), _ptr(gates), T, k, D, y.shape[0], _ptr(dy), _ptr(dgates))
+    return _call("csf_combine_backward", args, (dy, dgates), dev, (dout, y, slots, gates), (dy, dgates), stream)
 
 
 def _route_backward(dgates, logits, experts, gates, renorm=True, stream=None) -> Bound:
@@ -240,11 +252,10 @@ def _route_backward(dgates, logits, experts, gates, renorm=True, stream=None) ->
         raise ValueError(f"{where}: experts must be [{T}, topk], topk at most min(E, 64), E at most {MAX_EXPERTS}")
     _need(where, "dgates", dgates, (torch.float32,), dev, T * k)
     _need(where, "gates", gates, (torch.float32,), dev, T * k)
-    handle, side = _enter(stream, dev)
     dlogits = torch.empty_like(logits)
     args = (DTYPES[logits.dtype], _ptr(dgates), _ptr(logits), _ptr(experts), _ptr(gates), T, E, k, int(bool(renorm)),
-            _ptr(dlogits), handle)
-    return _call("csf_route_backward", args, dlogits, dev, (dgates, logits, experts, gates), (dlogits,), side)
+            _ptr(dlogits))
+    return _call("csf_route_backward", args, dlogits, dev, (dgates, logits, experts, gates), (dlogits,), stream)
 
 
 def _gated_shapes(where, scales, weights, alpha, expert_start):
@@ -286,7 +297,6 @@ def _moe_gated(scales, weights, x, alpha, expert_start, rows, x_scales=None, sav
     S = rows.shape[0]
     if dense_scales is not None:
         _dense(where, scales, dense_scales, dev)
-    handle, side = _enter(stream, dev)
     h = torch.empty(S, F, dtype=torch.bfloat16, device=dev)
     gu = torch.empty(S, 2 * F, dtype=torch.bfloat16, device=dev) if save else None
     d = scales.descriptor()
@@ -295,9 +305,9 @@ def _moe_gated(scales, weights, x, alpha, expert_start, rows, x_scales=None, sav
         need = min(need, 64)
     workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     args = (ctypes.byref(d), _ptr(dense_scales), weights.data_ptr(), _ptr(x), _ptr(x_scales), T, alpha.data_ptr(),
-            expert_start.data_ptr(), _ptr(rows), S, _ptr(h), _ptr(gu), _ptr(workspace), need, handle)
+            expert_start.data_ptr(), _ptr(rows), S, _ptr(h), _ptr(gu), _ptr(workspace), need)
     inputs = (scales, d, weights, x, x_scales, alpha, expert_start, rows, dense_scales)
-    return _call("csf_moe_gated", args, (h, gu) if save else h, dev, inputs, (h, gu, workspace), side)
+    return _call("csf_moe_gated", args, (h, gu) if save else h, dev, inputs, (h, gu, workspace), stream)
 
 
 def _moe_gated_backward(scales, dense_scales, weights, dh, gate_up, alpha, expert_start, stream=None) -> Bound:
@@ -309,14 +319,13 @@ def _moe_gated_backward(scales, dense_scales, weights, dh, gate_up, alpha, exper
     if dh.shape[1] != F:
         raise ValueError(f"{where}: dh must be [S, {F}]")
     _need(where, "gate_up", gate_up, (torch.bfloat16,), dev, S * 2 * F)
-    handle, side = _enter(stream, dev)
     dx = torch.empty(S, K, dtype=torch.bfloat16, device=dev)
     dgu = torch.empty(S, 2 * F, dtype=torch.bfloat16, device=dev)
     d = scales.descriptor()
     args = (ctypes.byref(d), dense_scales.data_ptr(), weights.data_ptr(), _ptr(dh), _ptr(gate_up), S, alpha.data_ptr(),
-            expert_start.data_ptr(), _ptr(dx), _ptr(dgu), handle)
+            expert_start.data_ptr(), _ptr(dx), _ptr(dgu))
     inputs = (scales, d, dense_scales, weights, dh, gate_up, alpha, expert_start)
-    return _call("csf_moe_gated_backward", args, (dx, dgu), dev, inputs, (dx, dgu), side)
+    return _call("csf_moe_gated_backward", args, (dx, dgu), dev, inputs, (dx, dgu), stream)
 
 
 def rms_norm(x, weight, residual=None, slots=None, gates=None, eps=1e-6, mxfp8=False, stream=None) -> Normed:
@@ -377,8 +386,9 @@ _BINDERS = {rms_norm: _rms_norm, rms_norm_backward: _rms_norm_backward, route: _
 
 def bound(function, *args, **kwargs) -> Bound:
     """One call of a layer operator, checked and marshalled once: each call of the
-    result enqueues it again on the same buffers (and on the stream it was bound
-    on) and returns the same outputs.  Keeps references to every tensor."""
+    result enqueues it again on the same buffers and returns the same outputs, on
+    the stream then current, or on ``stream`` where one is given here.  Keeps
+    references to every tensor; a graph that captured it needs it kept."""
     if function not in _BINDERS:
         raise ValueError("bound() takes one of: " + ", ".join(f.__name__ for f in _BINDERS))
     return _BINDERS[function](*args, **kwargs)

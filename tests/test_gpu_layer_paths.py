@@ -120,3 +120,56 @@ def test_inputs_dropped_after_a_call_on_another_stream(dev):
         side.synchronize()
         assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
         del junk
+
+
+def test_bound_calls_captured_later_and_on_another_stream(dev):
+    """Calls bound before a capture land in its graph; calls bound on a stream
+    wait for the inputs that the current stream wrote since the last one."""
+    rng = np.random.default_rng(23)
+    T, E, k = 70, 6, 2
+    c = Gated(E, 48, 256, [1] * E, workloads.NVFP4, seed=24)
+    w = 1.0 + normal(rng, c.K, scale=0.1)
+    x, logits = normal(rng, T, c.K, dtype=torch.bfloat16), normal(rng, T, E)
+
+    def bind(**kw):
+        norm = csf.bound(csf.rms_norm, x, w, x, **kw)
+        route = csf.bound(csf.route, logits, k, **kw)
+        n, r = norm(), route()
+        return norm, route, csf.bound(csf.moe_gated, c.stack, c.tw, n.out, c.ta, r.expert_start, r.rows, **kw)
+
+    def plain():
+        n, r = csf.rms_norm(x, w, x), csf.route(logits, k)
+        return n, r, csf.moe_gated(c.stack, c.tw, n.out, c.ta, r.expert_start, r.rows)
+
+    def renew():
+        x.copy_(normal(rng, T, c.K, dtype=torch.bfloat16))
+        logits.copy_(normal(rng, T, E))
+
+    def same(got, want):
+        assert torch.equal(got[0].out, want[0].out) and torch.equal(got[0].sum, want[0].sum)
+        assert all(torch.equal(a, b) for a, b in zip(got[1], want[1])) and torch.equal(got[2], want[2])
+
+    calls = bind()
+    [call() for call in calls]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = [call() for call in calls]
+    for _ in range(4):
+        renew()
+        want = plain()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        same(out, want)
+    side = torch.cuda.Stream()
+    calls = bind(stream=side)
+    big = torch.empty(64 << 20, dtype=torch.float32, device=dev)
+    for _ in range(4):
+        torch.cuda.current_stream().wait_stream(side)  # the last call has read its inputs
+        for i in range(10):  # a few milliseconds before the inputs change
+            big.fill_(float(i))
+        renew()
+        out = [call() for call in calls]
+        torch.cuda.current_stream().wait_stream(side)
+        same(out, plain())
