@@ -451,10 +451,8 @@ csf_status csf_route_backward(int32_t dtype, const float *dgates, const void *lo
  *   the backward pass reads), or NULL.  Rows of slots outside every expert's
  *   range are not written.
  * No factor is rounded, and products are summed in float32 (MXFP4 weights with
- * scale bytes 0, 1, 253 or 254 and bfloat16 x follow the hardware's conversion;
- * with 8-bit x the matrix instruction's own sums over 128 products are off by up
- * to about 2^-16 of the terms' magnitudes); h is computed from the unrounded g
- * and u.
+ * scale bytes 0, 1, 253 or 254 and bfloat16 x follow the hardware's conversion);
+ * h is computed from the unrounded g and u.
  * workspace: with 20 or more slots per expert its first 64 bytes deal out the
  *   kernel's tiles and the rest holds decoded scales; with dense_scales it may be
  *   NULL or just those 64 bytes (without them the tiles are dealt out in turn,

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import workloads
-from test_gpu_layer import U, Gated, f64, near, normal
+from test_gpu_layer import U, Gated, check_gated, f64, near, normal
 
 csf = pytest.importorskip("moe_weight_decode_amd")
 
@@ -73,6 +73,45 @@ def test_gated_backward_of_millions_of_rows(dev):
     gu[120] = float("nan")
     bad, _ = backward()
     assert bad[120].isnan().all() and torch.equal(bad[:120], dx[:120]) and torch.equal(bad[121:], dx[121:])
+
+
+# ------------------------------------------------------------------ 8-bit activations
+
+def any_codes(rng, c: Gated):
+    """Every E4M3 code but NaN alike often, the scales 2^-5 .. 2^5: products of one
+    sum that lie up to 2^22 apart, and their sums often near 0."""
+    T = c.x.shape[0]
+    codes = rng.integers(0, 256, (T, c.K)).astype(np.uint8)
+    codes[codes & 0x7f == 0x7f] = 0
+    scales = rng.integers(122, 133, (T, c.K // 32)).astype(np.uint8)
+    c.x, c.xs = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    c.x64 = f64(c.x.view(torch.float8_e4m3fn).float()) * np.repeat(2.0 ** (scales.astype(np.float64) - 127), 32, axis=1)
+    return c
+
+
+@pytest.mark.parametrize("E,F,K,counts", [
+    (2, 40, 32, [3, 16]), (2, 200, 32, [130, 90]),              # few slots, many
+    (3, 33, 160, [7, 0, 18]), (2, 129, 160, [257, 20]),
+    (8, 16, 2048, [1, 2, 0, 3, 1, 1, 17, 5]), (1, 64, 2048, [64]),
+    (2, 24, 5120, [4, 19]), (1, 20, 8192, [31]),
+])
+def test_sums_of_any_8_bit_codes_are_as_in_float32(dev, E, F, K, counts):
+    rng = np.random.default_rng(E + F + K)
+    c = any_codes(rng, Gated(E, F, K, counts, workloads.MXFP4, True, seed=F + K))
+    h, gu = c.forward(save=True)
+    check_gated(c, h, gu)
+
+
+def test_many_experts_by_tiles_with_8_bit_activations(dev):
+    rng = np.random.default_rng(8)
+    counts = rng.integers(0, 45, 700)
+    counts[[0, 3, 4, 5, 699]] = 0
+    counts[350] = 300
+    c = Gated(700, 9, 32, counts, workloads.MXFP4, True, seed=16)
+    for codes in (c, any_codes(rng, c)):
+        h, gu = codes.forward(save=True)
+        check_gated(codes, h, gu)
+        assert torch.equal(codes.forward(dense_scales=codes.dense()), h)
 
 
 # ------------------------------------------------------------------ streams and graphs
