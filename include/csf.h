@@ -472,10 +472,11 @@ csf_status csf_moe_gated(const csf_stack *scales, const uint8_t *dense_scales, c
  *     dgate_up[s] = (dh u p (1 + g (1 - p)), dh g p),
  *     dx[s] = alpha[e] * (dg W[e][0 .. F) + du W[e][F .. 2F))
  * per slot: dx is bfloat16 [num_slots][K]; a token's gradient is the sum of its
- * slots'.  The weights are frozen codes
- * and get no gradient.  dense_scales is needed (csf_decode with the same
- * expert_start fills it); of scales only the shape is used.  The products
- * take dgate_up as rounded to bfloat16.  dx is 16-byte aligned, dgate_up 4.
+ * slots'.  Rows of slots outside every expert's range are not written.  The
+ * weights are frozen codes and get no gradient.  dense_scales is needed
+ * (csf_decode with the same expert_start fills it); of scales only the shape is
+ * used.  The products take dgate_up as rounded to bfloat16.  dx is 16-byte
+ * aligned, dgate_up 4.
  */
 csf_status csf_moe_gated_backward(const csf_stack *scales, const uint8_t *dense_scales, const uint8_t *weights,
                                   const uint16_t *dh, const uint16_t *gate_up, int32_t num_slots, const float *alpha,

@@ -852,7 +852,7 @@ __global__ void csf_gated_queue_kernel(uint32_t *queue) {
 // dgu of every routed slot: a workgroup takes rows in turn.
 __global__ __launch_bounds__(kGatedThreads) void csf_gated_dgu_kernel(GatedBackwardArgs a) {
     const uint32_t F = a.F, used = (uint32_t)min(max(a.expert_start[a.E], 0), (int32_t)a.S);
-    for (uint32_t s = blockIdx.x; s < used; s += gridDim.x) {
+    for (uint32_t s = (uint32_t)max(a.expert_start[0], 0) + blockIdx.x; s < used; s += gridDim.x) {
         const __bf16 *gu = reinterpret_cast<const __bf16 *>(a.gu) + (uint64_t)s * 2u * F;
         const __bf16 *dh = reinterpret_cast<const __bf16 *>(a.dh) + (uint64_t)s * F;
         __bf16 *dgu = reinterpret_cast<__bf16 *>(a.dgu) + (uint64_t)s * 2u * F;

@@ -75,6 +75,26 @@ def test_gated_backward_of_millions_of_rows(dev):
     assert bad[120].isnan().all() and torch.equal(bad[:120], dx[:120]) and torch.equal(bad[121:], dx[121:])
 
 
+def test_gated_backward_writes_routed_slots_only(dev):
+    # routing of some of the experts, as of one device's: the slots before the first one's are others'
+    c = Gated(3, 40, 96, [4, 3, 9], workloads.NVFP4, seed=4)
+    S, first = len(c.rows), 4
+    _, gu = c.forward(save=True)
+    dh = normal(np.random.default_rng(5), S, c.F, dtype=torch.bfloat16)
+    want = csf.moe_gated_backward(c.stack, c.dense(), c.tw, dh, gu, c.ta, c.te)
+    es = c.te.clone()
+    es[0] = first  # expert 0 has no slots left
+    gu[:first] = float("nan")
+    d = c.stack.descriptor()
+    dx = torch.full((S, c.K), 7.0, dtype=torch.bfloat16, device=dev)
+    dgu = torch.full((S, 2 * c.F), 7.0, dtype=torch.bfloat16, device=dev)
+    assert csf.library().csf_moe_gated_backward(
+        ctypes.byref(d), c.dense().data_ptr(), c.tw.data_ptr(), dh.data_ptr(), gu.data_ptr(), S, c.ta.data_ptr(), es.data_ptr(),
+        dx.data_ptr(), dgu.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    for got, full in ((dx, want[0]), (dgu, want[1])):
+        assert (got[:first] == 7).all() and torch.equal(got[first:], full[first:])
+
+
 # ------------------------------------------------------------------ 8-bit activations
 
 def any_codes(rng, c: Gated):
