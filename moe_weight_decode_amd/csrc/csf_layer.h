@@ -27,6 +27,7 @@ struct NormArgs {
     int64_t x_rows;
     float eps;
     uint32_t T, D, k;
+    uint32_t first;          // first workgroup of the launch
 };
 
 struct NormBackwardArgs {
@@ -56,6 +57,7 @@ struct RouteArgs {
     uint32_t *base;          // workspace [groups][E]: entries of earlier workgroups per expert
     uint32_t *total;         // workspace [E]
     uint32_t T, E, k, renorm, groups;
+    uint32_t first;          // first workgroup of the launch
 };
 
 // Bytes between two workgroups' counts: whole 16-byte loads.
@@ -70,6 +72,7 @@ struct CombineBackwardArgs {
     float *dgates;           // [T][k]
     int64_t S;
     uint32_t T, D, k;
+    uint32_t first;          // first workgroup of the launch
 };
 
 struct RouteBackwardArgs {
@@ -79,6 +82,7 @@ struct RouteBackwardArgs {
     const float *gates;      // [T][k]
     void *dlogits;           // [T][E]
     uint32_t T, E, k, renorm;
+    uint32_t first;          // first workgroup of the launch
 };
 
 hipError_t launch_route(int32_t dtype, const RouteArgs &a, hipStream_t stream);

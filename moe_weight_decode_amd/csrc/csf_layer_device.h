@@ -8,6 +8,19 @@
 namespace csf {
 namespace {
 
+// A launch holds fewer than 2^32 threads, and a larger one runs in part without an
+// error: more workgroups than kGridMost (of up to 1024 threads) take several
+// launches, the first workgroup of each in a.first.
+constexpr uint32_t kGridMost = 1u << 21;
+
+template <typename Args, typename Launch>
+void launch_groups(Args a, uint32_t groups, Launch &&launch) {
+    for (a.first = 0; a.first < groups; a.first += kGridMost) {
+        const uint32_t left = groups - a.first;
+        launch(a, dim3(left < kGridMost ? left : kGridMost));
+    }
+}
+
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));

@@ -58,9 +58,9 @@ __device__ __forceinline__ uint32_t mx8_byte(float m) {
 template <typename T, uint32_t CHUNKS, uint32_t THREADS, bool COMBINE, bool MX>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void csf_norm_kernel(NormArgs a) {
     __shared__ float lds[THREADS / kWave];
-    uint32_t row = blockIdx.x, tid = threadIdx.x;
+    uint32_t row = a.first + blockIdx.x, tid = threadIdx.x;
     if constexpr (THREADS == kWave) {
-        row = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + threadIdx.x / kWave);
+        row = __builtin_amdgcn_readfirstlane(row * 4u + threadIdx.x / kWave);
         tid = threadIdx.x % kWave;
         if (row >= a.T) return;  // no barriers on this path
     }
@@ -234,16 +234,17 @@ __global__ __launch_bounds__(1024) void csf_norm_dweight_kernel(NormBackwardArgs
 }
 
 template <typename T, uint32_t CHUNKS, uint32_t THREADS>
-void start_norm(const NormArgs &a, hipStream_t stream) {
-    const uint32_t grid = THREADS == kWave ? (a.T + 3u) / 4u : a.T;
+void start_norm(const NormArgs &all, hipStream_t stream) {
     const dim3 block(THREADS < 256 ? 256 : THREADS);
-    if (a.slots != nullptr) {
-        if (a.scales != nullptr) hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, true, true>), dim3(grid), block, 0, stream, a);
-        else hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, true, false>), dim3(grid), block, 0, stream, a);
-    } else {
-        if (a.scales != nullptr) hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, false, true>), dim3(grid), block, 0, stream, a);
-        else hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, false, false>), dim3(grid), block, 0, stream, a);
-    }
+    launch_groups(all, THREADS == kWave ? (all.T + 3u) / 4u : all.T, [&](const NormArgs &a, dim3 grid) {
+        if (a.slots != nullptr) {
+            if (a.scales != nullptr) hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, true, true>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, true, false>), grid, block, 0, stream, a);
+        } else {
+            if (a.scales != nullptr) hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, false, true>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((csf_norm_kernel<T, CHUNKS, THREADS, false, false>), grid, block, 0, stream, a);
+        }
+    });
 }
 
 // Threads and chunks that cover the columns: a wave per row up to 1024

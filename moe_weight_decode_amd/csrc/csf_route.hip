@@ -126,7 +126,8 @@ __global__ __launch_bounds__(kRouteThreads) void csf_route_kernel(RouteArgs a) {
     int16_t *chosen = reinterpret_cast<int16_t *>(start + a.E);        // [64][k]
     const uint32_t waves = blockDim.x / kWave, sub = threadIdx.x % LANES;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t t0 = blockIdx.x * kRouteTokens, tokens = min(kRouteTokens, a.T - t0);
+    const uint32_t group = a.first + blockIdx.x, t0 = group * kRouteTokens;
+    const uint32_t tokens = min(kRouteTokens, a.T - t0);
     const uint32_t E = a.E, k = a.k;
     for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) mask[e] = 0;
     __syncthreads();
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(kRouteThreads) void csf_route_kernel(RouteArgs a) {
         }
     }
     __syncthreads();
-    const bool one = gridDim.x == 1;
+    const bool one = a.groups == 1;
     if (one) {
         // offsets of the experts: thread i owns experts i per .. i per + per - 1
         const uint32_t per = (E + blockDim.x - 1u) / blockDim.x, e0 = threadIdx.x * per;
@@ -215,7 +216,7 @@ __global__ __launch_bounds__(kRouteThreads) void csf_route_kernel(RouteArgs a) {
     } else {
         const uint32_t stride = route_stride(E);
         for (uint32_t e = threadIdx.x; e < stride; e += blockDim.x)
-            a.count[(uint64_t)blockIdx.x * stride + e] = e < E ? (uint8_t)__popcll(mask[e]) : 0u;
+            a.count[(uint64_t)group * stride + e] = e < E ? (uint8_t)__popcll(mask[e]) : 0u;
     }
     for (uint32_t i = threadIdx.x; i < tokens * k; i += blockDim.x) {
         const int32_t e = chosen[i];
@@ -265,7 +266,8 @@ template <bool SUM>
 __global__ __launch_bounds__(kRouteThreads) void csf_route_place_kernel(RouteArgs a) {
     extern __shared__ __align__(16) uint8_t dyn_lds[];
     __shared__ uint32_t s_scan[kRouteThreads / kWave];
-    const uint32_t E = a.E, k = a.k, t0 = blockIdx.x * kRouteTokens, tokens = min(kRouteTokens, a.T - t0);
+    const uint32_t group = a.first + blockIdx.x, t0 = group * kRouteTokens;
+    const uint32_t E = a.E, k = a.k, tokens = min(kRouteTokens, a.T - t0);
     const uint32_t stride = route_stride(E);
     uint32_t *total = reinterpret_cast<uint32_t *>(dyn_lds), *start = total + stride;  // [stride] each
     const uint32_t tid = threadIdx.x;
@@ -289,7 +291,7 @@ __global__ __launch_bounds__(kRouteThreads) void csf_route_place_kernel(RouteArg
 #pragma unroll
                 for (uint32_t i = 0; i < kRouteSumGroups / kWave; ++i) {
                     const uint32_t lo = v[i][w] & 0x00ff00ffu, hi = (v[i][w] >> 8) & 0x00ff00ffu;
-                    const bool before = lane + kWave * i < blockIdx.x;
+                    const bool before = lane + kWave * i < group;
                     even += lo, odd += hi;
                     even_before += before ? lo : 0u, odd_before += before ? hi : 0u;
                 }
@@ -304,7 +306,7 @@ __global__ __launch_bounds__(kRouteThreads) void csf_route_place_kernel(RouteArg
     } else {
         for (uint32_t e = tid; e < E; e += kRouteThreads) {
             total[e] = a.total[e];
-            start[e] = a.base[(uint64_t)blockIdx.x * E + e];
+            start[e] = a.base[(uint64_t)group * E + e];
         }
     }
     __syncthreads();
@@ -314,10 +316,10 @@ __global__ __launch_bounds__(kRouteThreads) void csf_route_place_kernel(RouteArg
     uint32_t at = exclusive_scan(sum, s_scan, all);
     for (uint32_t i = 0; i < per && e0 + i < E; ++i) {
         start[e0 + i] += at;
-        if (blockIdx.x == 0) a.expert_start[e0 + i] = (int32_t)at;
+        if (group == 0) a.expert_start[e0 + i] = (int32_t)at;
         at += total[e0 + i];
     }
-    if (blockIdx.x == 0 && tid == 0) a.expert_start[E] = (int32_t)all;
+    if (group == 0 && tid == 0) a.expert_start[E] = (int32_t)all;
     __syncthreads();
     for (uint32_t i = tid; i < tokens * k; i += kRouteThreads) {
         const uint64_t at_choice = choice + i;
@@ -335,7 +337,7 @@ __global__ __launch_bounds__(kRouteThreads) void csf_route_place_kernel(RouteArg
 template <typename T>
 __global__ __launch_bounds__(256) void csf_combine_backward_kernel(CombineBackwardArgs a) {
     const uint32_t lane = threadIdx.x % kWave;
-    const uint32_t t = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + threadIdx.x / kWave);
+    const uint32_t t = __builtin_amdgcn_readfirstlane((a.first + blockIdx.x) * 4u + threadIdx.x / kWave);
     if (t >= a.T) return;
     const uint32_t D = a.D;
     const T *dout = static_cast<const T *>(a.dout) + (uint64_t)t * D;
@@ -372,7 +374,7 @@ __global__ __launch_bounds__(256) void csf_route_backward_kernel(RouteBackwardAr
     __shared__ __align__(16) float s_added[4][kWave * EPL];
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     float *added = s_added[wave];  // the chosen experts' p_e (dg_e - ..)
-    const uint32_t t = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + wave);
+    const uint32_t t = __builtin_amdgcn_readfirstlane((a.first + blockIdx.x) * 4u + wave);
     if (t >= a.T) return;  // no barriers: a wave's LDS row is its own
     const uint32_t E = a.E, k = a.k, first = lane * EPL, left = first < E ? E - first : 0u;
     const uint64_t row = (uint64_t)t * E;
@@ -424,8 +426,10 @@ __global__ __launch_bounds__(256) void csf_route_backward_kernel(RouteBackwardAr
 }
 
 template <typename T, uint32_t LANES, uint32_t EPL>
-void start_route(const RouteArgs &a, uint32_t threads, size_t lds, hipStream_t stream) {
-    hipLaunchKernelGGL((csf_route_kernel<T, LANES, EPL>), dim3(a.groups), dim3(threads), lds, stream, a);
+void start_route(const RouteArgs &all, uint32_t threads, size_t lds, hipStream_t stream) {
+    launch_groups(all, all.groups, [&](const RouteArgs &a, dim3 grid) {
+        hipLaunchKernelGGL((csf_route_kernel<T, LANES, EPL>), grid, dim3(threads), lds, stream, a);
+    });
 }
 
 template <typename T>
@@ -456,7 +460,9 @@ void pick_route(const RouteArgs &a, hipStream_t stream) {
             hipLaunchKernelGGL(csf_route_place_kernel<true>, dim3(a.groups), dim3(kRouteThreads), place, stream, a);
         } else {
             hipLaunchKernelGGL(csf_route_offsets_kernel, dim3((a.E + kWave - 1u) / kWave), dim3(kRouteThreads), 0, stream, a);
-            hipLaunchKernelGGL(csf_route_place_kernel<false>, dim3(a.groups), dim3(kRouteThreads), place, stream, a);
+            launch_groups(a, a.groups, [&](const RouteArgs &part, dim3 grid) {
+                hipLaunchKernelGGL(csf_route_place_kernel<false>, grid, dim3(kRouteThreads), place, stream, part);
+            });
         }
     }
 }
@@ -470,24 +476,28 @@ hipError_t launch_route(int32_t dtype, const RouteArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_combine_backward(int32_t dtype, const CombineBackwardArgs &a, hipStream_t stream) {
-    const dim3 grid((a.T + 3u) / 4u), block(256);
-    if (dtype == kBF16) hipLaunchKernelGGL(csf_combine_backward_kernel<__bf16>, grid, block, 0, stream, a);
-    else if (dtype == kF16) hipLaunchKernelGGL(csf_combine_backward_kernel<_Float16>, grid, block, 0, stream, a);
-    else hipLaunchKernelGGL(csf_combine_backward_kernel<float>, grid, block, 0, stream, a);
+hipError_t launch_combine_backward(int32_t dtype, const CombineBackwardArgs &all, hipStream_t stream) {
+    const dim3 block(256);
+    launch_groups(all, (all.T + 3u) / 4u, [&](const CombineBackwardArgs &a, dim3 grid) {
+        if (dtype == kBF16) hipLaunchKernelGGL(csf_combine_backward_kernel<__bf16>, grid, block, 0, stream, a);
+        else if (dtype == kF16) hipLaunchKernelGGL(csf_combine_backward_kernel<_Float16>, grid, block, 0, stream, a);
+        else hipLaunchKernelGGL(csf_combine_backward_kernel<float>, grid, block, 0, stream, a);
+    });
     return hipGetLastError();
 }
 
 template <typename T>
-static void pick_route_backward(const RouteBackwardArgs &a, hipStream_t stream) {
-    const dim3 grid((a.T + 3u) / 4u), block(256);
-    const uint32_t epl = (a.E + kWave - 1u) / kWave;
-    if (epl <= 1) hipLaunchKernelGGL((csf_route_backward_kernel<T, 1>), grid, block, 0, stream, a);
-    else if (epl <= 2) hipLaunchKernelGGL((csf_route_backward_kernel<T, 2>), grid, block, 0, stream, a);
-    else if (epl <= 4) hipLaunchKernelGGL((csf_route_backward_kernel<T, 4>), grid, block, 0, stream, a);
-    else if (epl <= 8) hipLaunchKernelGGL((csf_route_backward_kernel<T, 8>), grid, block, 0, stream, a);
-    else if (epl <= 16) hipLaunchKernelGGL((csf_route_backward_kernel<T, 16>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((csf_route_backward_kernel<T, 32>), grid, block, 0, stream, a);
+static void pick_route_backward(const RouteBackwardArgs &all, hipStream_t stream) {
+    const dim3 block(256);
+    const uint32_t epl = (all.E + kWave - 1u) / kWave;
+    launch_groups(all, (all.T + 3u) / 4u, [&](const RouteBackwardArgs &a, dim3 grid) {
+        if (epl <= 1) hipLaunchKernelGGL((csf_route_backward_kernel<T, 1>), grid, block, 0, stream, a);
+        else if (epl <= 2) hipLaunchKernelGGL((csf_route_backward_kernel<T, 2>), grid, block, 0, stream, a);
+        else if (epl <= 4) hipLaunchKernelGGL((csf_route_backward_kernel<T, 4>), grid, block, 0, stream, a);
+        else if (epl <= 8) hipLaunchKernelGGL((csf_route_backward_kernel<T, 8>), grid, block, 0, stream, a);
+        else if (epl <= 16) hipLaunchKernelGGL((csf_route_backward_kernel<T, 16>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((csf_route_backward_kernel<T, 32>), grid, block, 0, stream, a);
+    });
 }
 
 hipError_t launch_route_backward(int32_t dtype, const RouteBackwardArgs &a, hipStream_t stream) {

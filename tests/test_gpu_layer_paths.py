@@ -95,6 +95,81 @@ def test_gated_backward_writes_routed_slots_only(dev):
         assert (got[:first] == 7).all() and torch.equal(got[first:], full[first:])
 
 
+# ------------------------------------------------------------------ launches past 2^32 threads
+
+MANY = 2 ** 26 + 5  # tokens of a wave each
+
+
+def ends(T):
+    """Tokens at both ends and around the first that a launch of one axis would not reach."""
+    return [slice(0, 300), slice(2 ** 26 - 150, min(T, 2 ** 26 + 150)), slice(T - 300, T)]
+
+
+def test_norm_of_more_tokens_than_a_launch_axis_holds(dev):
+    g = torch.Generator(device=dev)
+    g.manual_seed(6)
+    x = torch.randn(MANY, 4, generator=g, device=dev, dtype=torch.bfloat16)
+    w = torch.tensor([0.5, 1.0, 2.0, 3.0], device=dev)
+    r = csf.rms_norm(x, w)
+    for s in ends(MANY):
+        want = csf.rms_norm(x[s].contiguous(), w)
+        assert torch.equal(r.out[s], want.out) and torch.equal(r.rstd[s], want.rstd)
+    assert (r.rstd > 0).all()
+
+
+def test_norm_of_more_long_rows_than_a_launch_axis_holds(dev):
+    # a workgroup a row: 2^24 rows of 256 threads; the sums of few experts' outputs, as 8 bits, to keep it small
+    T, D, S = 2 ** 24 + 3, 1025, 5
+    rng = np.random.default_rng(7)
+    x, w, gates = normal(rng, S, D), 1.0 + normal(rng, D, scale=0.1), torch.ones(T, 1, device=dev)
+    slots = (torch.arange(T, dtype=torch.int32, device=dev) % S)[:, None].contiguous()
+    out = torch.zeros(T, D, dtype=torch.uint8, device=dev)
+    scales, rstd = torch.zeros(T, 33, dtype=torch.uint8, device=dev), torch.zeros(T, device=dev)
+    assert csf.library().csf_rms_norm(0, x.data_ptr(), None, w.data_ptr(), T, D, slots.data_ptr(), gates.data_ptr(), 1, S, 1e-6,
+                                      None, out.data_ptr(), scales.data_ptr(), rstd.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream) == 0
+    want = csf.rms_norm(x, w, mxfp8=True)
+    assert torch.equal(rstd, want.rstd[slots[:, 0].long()])
+    for at in (0, 2 ** 24 - 5, T - 5):
+        k = slots[at:at + 5, 0].long()
+        assert torch.equal(out[at:at + 5], want.out[k]) and torch.equal(scales[at:at + 5], want.scales[k])
+
+
+def test_route_and_gradients_of_more_tokens_than_a_launch_axis_holds(dev):
+    g = torch.Generator(device=dev)
+    g.manual_seed(8)
+    logits = torch.randn(MANY, 2, generator=g, device=dev)
+    y, dout = torch.randn(MANY, 2, generator=g, device=dev), torch.randn(MANY, 2, generator=g, device=dev, dtype=torch.bfloat16)
+    slots = torch.arange(MANY, dtype=torch.int32, device=dev)[:, None].contiguous()
+    gates = torch.rand(MANY, 1, generator=g, device=dev)
+    dy, dg = csf.combine_backward(dout, y, slots, gates)
+    experts = (logits[:, :1] < logits[:, 1:]).to(torch.int32)
+    dl = csf.route_backward(dg, logits, experts, gates, renorm=False)
+    for s in ends(MANY):
+        n = s.stop - s.start
+        want = csf.combine_backward(dout[s].contiguous(), y[s].contiguous(), slots[:n].contiguous(), gates[s].contiguous())
+        assert torch.equal(dy[s], want[0]) and torch.equal(dg[s], want[1])
+        want = csf.route_backward(dg[s].contiguous(), logits[s].contiguous(), experts[s].contiguous(), gates[s].contiguous(), renorm=False)
+        assert torch.equal(dl[s], want)
+
+
+def test_route_of_more_tokens_than_a_launch_axis_holds(dev):
+    # 1024 threads for 64 tokens
+    T = 2 ** 28 + 70
+    g = torch.Generator(device=dev)
+    g.manual_seed(9)
+    logits = torch.randn(T, 2, generator=g, device=dev, dtype=torch.bfloat16)
+    r = csf.route(logits, 1)
+    second = logits[:, 0] < logits[:, 1]
+    assert torch.equal(r.experts[:, 0], second.to(torch.int32)) and (r.gates == 1).all()
+    zeros = T - int(second.sum())
+    assert r.expert_start.tolist() == [0, zeros, T]
+    token = torch.arange(T, dtype=torch.int32, device=dev)
+    order = torch.cat((token[~second], token[second]))
+    assert torch.equal(r.rows, order)
+    assert torch.equal(r.slots[order.long(), 0], token)
+
+
 # ------------------------------------------------------------------ 8-bit activations
 
 def any_codes(rng, c: Gated):
