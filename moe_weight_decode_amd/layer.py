@@ -2,7 +2,7 @@
 feed-forward half and their backward passes (``include/csf.h``).
 
 Argument marshalling only, as the rest of the binding.  Every function checks
-its tensors (device, type, size, contiguity), allocates its outputs and its
+its tensors (device, type, shape, contiguity), allocates its outputs and its
 workspace, enqueues on ``stream`` (default: the current one) and returns
 without synchronising.  A ``stream`` other than the current one first waits for
 the current stream's queued work, since the inputs may come from it and the
@@ -112,10 +112,10 @@ class Bound:
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _need(where: str, name: str, t, dtypes, dev, numel=None, dim=None):
+def _need(where: str, name: str, t, dtypes, dev, numel=None, dim=None, shape=None):
     if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype not in dtypes or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous {' or '.join(map(str, dtypes))} tensor on {dev}")
-    if (numel is not None and t.numel() != numel) or (dim is not None and t.dim() != dim):
+    if (numel is not None and t.numel() != numel) or (dim is not None and t.dim() != dim) or (shape is not None and t.shape != shape):
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, which does not match the call")
 
 
@@ -166,7 +166,7 @@ def _rms_norm(x, weight, residual=None, slots=None, gates=None, eps=1e-6, mxfp8=
         _need(where, "x (the experts' outputs)", x, (torch.float32,), dev)
         _need(where, "slots", slots, (torch.int32,), dev, dim=2)
         T, k = slots.shape
-        _need(where, "gates", gates, (torch.float32,), dev, T * k)
+        _need(where, "gates", gates, (torch.float32,), dev, shape=(T, k))
         if residual is None:
             raise ValueError(f"{where}: the combination needs the residual")
     else:
@@ -176,7 +176,7 @@ def _rms_norm(x, weight, residual=None, slots=None, gates=None, eps=1e-6, mxfp8=
             raise ValueError(f"{where}: gates without slots")
     dtype = x.dtype if residual is None else getattr(residual, "dtype", None)
     if residual is not None:
-        _need(where, "residual", residual, tuple(DTYPES) if slots is not None else (x.dtype,), dev, T * D)
+        _need(where, "residual", residual, tuple(DTYPES) if slots is not None else (x.dtype,), dev, shape=(T, D))
     _need(where, "weight", weight, (torch.float32,), dev, D)
     total = x if residual is None else torch.empty(T, D, dtype=dtype, device=dev)
     out = torch.empty(T, D, dtype=torch.uint8 if mxfp8 else dtype, device=dev)
@@ -193,11 +193,11 @@ def _rms_norm_backward(dy, sum, weight, rstd, dsum=None, stream=None) -> Bound:
     dev = _device(where, dy, "dy")
     _need(where, "dy", dy, tuple(DTYPES), dev, dim=2)
     T, D = dy.shape
-    _need(where, "sum", sum, (dy.dtype,), dev, T * D)
+    _need(where, "sum", sum, (dy.dtype,), dev, shape=(T, D))
     _need(where, "weight", weight, (torch.float32,), dev, D)
     _need(where, "rstd", rstd, (torch.float32,), dev, T)
     if dsum is not None:
-        _need(where, "dsum", dsum, (dy.dtype,), dev, T * D)
+        _need(where, "dsum", dsum, (dy.dtype,), dev, shape=(T, D))
     dx = torch.empty_like(dy)
     dweight = torch.empty(D, dtype=torch.float32, device=dev)
     need = _lib().csf_rms_norm_backward_workspace(T, D)
@@ -234,7 +234,7 @@ def _combine_backward(dout, y, slots, gates, stream=None) -> Bound:
     k = slots.shape[1]
     if y.shape[1] != D or slots.shape[0] != T or k < 1:
         raise ValueError(f"{where}: y must be [S, {D}] and slots [{T}, k]")
-    _need(where, "gates", gates, (torch.float32,), dev, T * k)
+    _need(where, "gates", gates, (torch.float32,), dev, shape=(T, k))
     dy = torch.empty(y.shape, dtype=dout.dtype, device=dev)
     dgates = torch.empty(T, k, dtype=torch.float32, device=dev)
     args = (DTYPES[dout.dtype], _ptr(dout), _ptr(y), _ptr(slots), _ptr(gates), T, k, D, y.shape[0], _ptr(dy), _ptr(dgates))
@@ -250,8 +250,8 @@ def _route_backward(dgates, logits, experts, gates, renorm=True, stream=None) ->
     k = experts.shape[1]
     if experts.shape[0] != T or not 1 <= k <= min(E, 64) or E > MAX_EXPERTS:
         raise ValueError(f"{where}: experts must be [{T}, topk], topk at most min(E, 64), E at most {MAX_EXPERTS}")
-    _need(where, "dgates", dgates, (torch.float32,), dev, T * k)
-    _need(where, "gates", gates, (torch.float32,), dev, T * k)
+    _need(where, "dgates", dgates, (torch.float32,), dev, shape=(T, k))
+    _need(where, "gates", gates, (torch.float32,), dev, shape=(T, k))
     dlogits = torch.empty_like(logits)
     args = (DTYPES[logits.dtype], _ptr(dgates), _ptr(logits), _ptr(experts), _ptr(gates), T, E, k, int(bool(renorm)),
             _ptr(dlogits))
@@ -289,7 +289,7 @@ def _moe_gated(scales, weights, x, alpha, expert_start, rows, x_scales=None, sav
         _need(where, "x (E4M3 codes)", x, (torch.uint8,), dev, dim=2)
         if scales.fmt != MXFP4:
             raise ValueError(f"{where}: 8-bit activations need MXFP4 weights")
-        _need(where, "x_scales", x_scales, (torch.uint8,), dev, x.shape[0] * (K // 32))
+        _need(where, "x_scales", x_scales, (torch.uint8,), dev, shape=(x.shape[0], K // 32))
     T = x.shape[0]
     if x.shape[1] != K:
         raise ValueError(f"{where}: x must be [T, {K}]")
@@ -318,7 +318,7 @@ def _moe_gated_backward(scales, dense_scales, weights, dh, gate_up, alpha, exper
     S = dh.shape[0]
     if dh.shape[1] != F:
         raise ValueError(f"{where}: dh must be [S, {F}]")
-    _need(where, "gate_up", gate_up, (torch.bfloat16,), dev, S * 2 * F)
+    _need(where, "gate_up", gate_up, (torch.bfloat16,), dev, shape=(S, 2 * F))
     dx = torch.empty(S, K, dtype=torch.bfloat16, device=dev)
     dgu = torch.empty(S, 2 * F, dtype=torch.bfloat16, device=dev)
     d = scales.descriptor()

@@ -109,3 +109,20 @@ def test_a_bound_call_on_a_stream_waits_every_time(machine):
         assert side.waits == 3 and machine.calls == [2, 2, 2, 2]
         machine.now = 1
         machine.calls.clear()
+
+
+def test_transposed_tensors_are_refused(machine):
+    """As many elements in another order are no match: rows would be taken for columns."""
+    i = torch.int32
+    x, w, r, slots, gates = new(4, 64), new(64), new(4), new(4, 2, dtype=i), new(4, 2)
+    turned, turned2 = new(64, 4), new(2, 4)
+    for call in (lambda: csf.rms_norm(x, w, turned),
+                 lambda: csf.rms_norm(new(8, 64), w, x, slots=slots, gates=turned2),
+                 lambda: csf.rms_norm_backward(x, turned, w, r),
+                 lambda: csf.rms_norm_backward(x, x, w, r, turned),
+                 lambda: csf.combine_backward(x, new(8, 64), slots, turned2),
+                 lambda: csf.route_backward(turned2, new(4, 16), slots, gates),
+                 lambda: csf.route_backward(gates, new(4, 16), slots, turned2)):
+        with pytest.raises(ValueError, match="shape"):
+            call()
+    assert machine.calls == []
