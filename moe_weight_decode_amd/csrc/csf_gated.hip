@@ -120,8 +120,8 @@ __device__ __forceinline__ v2f sigmoid2(float g) {
 // codes (all of a wave's share of K), the scales' streams,
 // the slots' tokens; the exceptions once the tile index is in; the first
 // activations once the tokens are.  The scales are expanded in LDS meanwhile.
-// The waves take every eighth chunk of K, their sums meet in LDS and are added
-// in the waves' order.  Several workgroups per compute unit cover each other's
+// The waves take every eighth chunk of K, NCH of them each (they cover it), their
+// sums meet in LDS and are added in the waves' order.  Several workgroups per compute unit cover each other's
 // round trips.
 
 // 16 scale bytes of run `pos` (a multiple of 16) of a plane, from its offset
@@ -139,6 +139,8 @@ __device__ __forceinline__ u32x4 expand_run(const StackArgs &st, u32x4 group, ui
 
 constexpr uint32_t kUnitWaves = 8;       // the vector work of widening a unit's weights is spread over 8 waves
 constexpr uint32_t kUnitThreads = kUnitWaves * kWave;
+constexpr uint32_t kUnitChunks = 8;      // chunks of a wave, at most
+static_assert(kUnitChunks * kUnitWaves * kGatedChunk >= kGatedMaxK, "a unit's waves hold all of K");
 constexpr uint32_t kUnitBases = 2u * kGatedCols + kBasesSlack;  // row bases of a half's span, its neighbours among them
 
 template <bool MX, bool X8, bool DENSE, uint32_t NCH>
@@ -199,16 +201,13 @@ __global__ __launch_bounds__(kUnitThreads, NCH > 4 ? 2 : 4) void csf_gated_unit_
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) rw[h] = make_rsrc(a.w + ((uint64_t)e * 2u * F + h * F + n0) * (K / 2u), cols * (K / 2u));
         u32x4 codes[NCH][2];
-        auto load_codes = [&](uint32_t kb) {
 #pragma unroll
-            for (uint32_t c = 0; c < NCH; ++c) {
-                const uint32_t k = kb + c * STRIDE + wave * kGatedChunk + 32u * kq;
-                const uint32_t off = k < K ? row * (K / 2u) + k / 2u : 0x80000000u;
+        for (uint32_t c = 0; c < NCH; ++c) {
+            const uint32_t k = c * STRIDE + wave * kGatedChunk + 32u * kq;
+            const uint32_t off = k < K ? row * (K / 2u) + k / 2u : 0x80000000u;
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) codes[c][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw[h], (int)off, 0, kNonTemporal));
-            }
-        };
-        load_codes(0u);
+            for (uint32_t h = 0; h < 2; ++h) codes[c][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw[h], (int)off, 0, kNonTemporal));
+        }
         // ---- scale bytes of the unit's rows into LDS
         if constexpr (DENSE) {
 #pragma unroll
@@ -253,28 +252,41 @@ __global__ __launch_bounds__(kUnitThreads, NCH > 4 ? 2 : 4) void csf_gated_unit_
                 }
         }
 
+                    constexpr uint32_t XV = X8 ? 2u : 4u;
+                    u32x4 x[2][XV];
+                    uint32_t xs[2];
+                    auto load_x = [&](uint32_t kc, auto bufc) {  // kc: the wave's chunk
+                        constexpr uint32_t BUF = decltype(bufc)::value;
+                        const u32x4 zero = {0u, 0u, 0u, 0u};
+                        if constexpr (X8) {
+                            // 8-bit operands: lane group q holds k = 16 q .. + 15 and 64 + 16 q .. + 15 of the chunk, but the
+                            // scale of block q, as 4-bit ones hold 32 q .. + 31
+                            const uint8_t *p = static_cast<const uint8_t *>(a.x) + at * K + kc + 16u * kq;
+                            x[BUF][0] = kc + 16u * kq < K ? *reinterpret_cast<const u32x4 *>(p) : zero;
+                            x[BUF][1] = kc + 64u + 16u * kq < K ? *reinterpret_cast<const u32x4 *>(p + 64) : zero;
+                            xs[BUF] = kc + 32u * kq < K ? a.x_scales[at * (K / 32u) + kc / 32u + kq] : 0u;
+                        } else {
+                            const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.x) + at * K + kc + 32u * kq);
+        #pragma unroll
+                            for (uint32_t s = 0; s < 4; ++s) x[BUF][s] = kc + 32u * kq < K ? p[s] : zero;
+                        }
+                    };
+        const std::integral_constant<uint32_t, 0> even;
+        const std::integral_constant<uint32_t, 1> odd;
+        uint32_t kc = wave * kGatedChunk;
+        load_x(kc, even);
+        __syncthreads();  // the scales are in LDS
         for (uint32_t tb = 0; tb < m; tb += 16u) {
-            if (tb > 0) at = token(tb + row);
-            v4f32 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            constexpr uint32_t XV = X8 ? 2u : 4u;
-            u32x4 x[2][XV];
-            uint32_t xs[2];
-            auto load_x = [&](uint32_t kc, auto bufc) {  // kc: the wave's chunk
-                constexpr uint32_t BUF = decltype(bufc)::value;
-                const u32x4 zero = {0u, 0u, 0u, 0u};
-                if constexpr (X8) {
-                    // 8-bit operands: lane group q holds k = 16 q .. + 15 and 64 + 16 q .. + 15 of the chunk, but the
-                    // scale of block q, as 4-bit ones hold 32 q .. + 31
-                    const uint8_t *p = static_cast<const uint8_t *>(a.x) + at * K + kc + 16u * kq;
-                    x[BUF][0] = kc + 16u * kq < K ? *reinterpret_cast<const u32x4 *>(p) : zero;
-                    x[BUF][1] = kc + 64u + 16u * kq < K ? *reinterpret_cast<const u32x4 *>(p + 64) : zero;
-                    xs[BUF] = kc + 32u * kq < K ? a.x_scales[at * (K / 32u) + kc / 32u + kq] : 0u;
-                } else {
-                    const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.x) + at * K + kc + 32u * kq);
+            // Widened anew for every 16 slots, and compared with K anew: kept from pass to pass, as the compiler would
+            // have it, the weights and the comparisons' results do not fit the registers.
+            asm volatile("" : "+s"(kc));
 #pragma unroll
-                    for (uint32_t s = 0; s < 4; ++s) x[BUF][s] = kc + 32u * kq < K ? p[s] : zero;
-                }
-            };
+            for (uint32_t c = 0; c < NCH; ++c) asm volatile("" : "+v"(codes[c][0]), "+v"(codes[c][1]));
+            if (tb > 0) {
+                at = token(tb + row);
+                load_x(kc, even);
+            }
+            v4f32 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
             auto products = [&](uint32_t kc, const u32x4 (&code)[2], auto bufc) {
                 constexpr uint32_t BUF = decltype(bufc)::value;
                 const uint32_t k = kc + 32u * kq;
@@ -302,21 +314,13 @@ __global__ __launch_bounds__(kUnitThreads, NCH > 4 ? 2 : 4) void csf_gated_unit_
                 }
                 __builtin_amdgcn_sched_barrier(0);
             };
-            const std::integral_constant<uint32_t, 0> even;
-            const std::integral_constant<uint32_t, 1> odd;
-            for (uint32_t kb = 0; kb < K; kb += NCH * STRIDE) {
-                if (K > NCH * STRIDE && (kb > 0 || tb > 0)) load_codes(kb);  // the first pass has the first ones
-                const uint32_t kc = kb + wave * kGatedChunk;
-                load_x(kc, even);
-                if (tb == 0 && kb == 0) __syncthreads();  // the scales are in LDS
 #pragma unroll
-                for (uint32_t c = 0; c < NCH; c += 2u) {
-                    if (c + 1u < NCH) load_x(kc + (c + 1u) * STRIDE, odd);
-                    products(kc + c * STRIDE, codes[c], even);
-                    if (c + 1u < NCH) {
-                        if (c + 2u < NCH) load_x(kc + (c + 2u) * STRIDE, even);
-                        products(kc + (c + 1u) * STRIDE, codes[c + 1u < NCH ? c + 1u : 0u], odd);
-                    }
+            for (uint32_t c = 0; c < NCH; c += 2u) {
+                if (c + 1u < NCH) load_x(kc + (c + 1u) * STRIDE, odd);
+                products(kc + c * STRIDE, codes[c], even);
+                if (c + 1u < NCH) {
+                    if (c + 2u < NCH) load_x(kc + (c + 2u) * STRIDE, even);
+                    products(kc + (c + 1u) * STRIDE, codes[c + 1u < NCH ? c + 1u : 0u], odd);
                 }
             }
 #pragma unroll
@@ -831,15 +835,10 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_tile_kernel(GatedA
             __syncthreads();  // the buffers are free for the next tile
         };
         switch (at.pairs) {
-            case 0: break;
             case 1: tile(std::integral_constant<uint32_t, 2>{}); break;
             case 2: tile(std::integral_constant<uint32_t, 4>{}); break;
             case 3: tile(std::integral_constant<uint32_t, 6>{}); break;
             default: tile(std::integral_constant<uint32_t, 8>{}); break;
-        }
-        if (at.pairs == 0 && a.queue != nullptr) {  // no expert's tile is empty; were one, the next is still asked for
-            if (tid == 0) s_next = q.settle(q.ask());
-            __syncthreads();
         }
         u = a.queue != nullptr ? __builtin_amdgcn_readfirstlane(s_next) : u + gridDim.x;
     }
@@ -1124,7 +1123,6 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_dx_kernel(GatedBac
             }
         };
         switch (at.pairs) {
-            case 0: break;
             case 1: tile(std::integral_constant<uint32_t, 2>{}); break;
             case 2: tile(std::integral_constant<uint32_t, 4>{}); break;
             case 3: tile(std::integral_constant<uint32_t, 6>{}); break;
@@ -1161,7 +1159,7 @@ static void start_units(const GatedArgs &a, hipStream_t stream) {
     if (chunks <= 1) hipLaunchKernelGGL((csf_gated_unit_kernel<MX, X8, DENSE, 1>), grid, block, lds, stream, a);
     else if (chunks <= 2) hipLaunchKernelGGL((csf_gated_unit_kernel<MX, X8, DENSE, 2>), grid, block, lds, stream, a);
     else if (chunks <= 4) hipLaunchKernelGGL((csf_gated_unit_kernel<MX, X8, DENSE, 4>), grid, block, lds, stream, a);
-    else hipLaunchKernelGGL((csf_gated_unit_kernel<MX, X8, DENSE, 8>), grid, block, lds, stream, a);
+    else hipLaunchKernelGGL((csf_gated_unit_kernel<MX, X8, DENSE, kUnitChunks>), grid, block, lds, stream, a);
 }
 
 hipError_t launch_gated(const GatedArgs &a, hipStream_t stream) {

@@ -9,6 +9,7 @@ namespace csf {
 
 constexpr uint32_t kCus = 256;             // compute units of an MI355X: grids are sized for them
 constexpr uint32_t kNormMaxCols = 32768;  // columns of a norm (a row is held in registers)
+constexpr uint32_t kGatedMaxK = 8192;     // columns of a gated projection's weights
 constexpr uint32_t kRouteMaxTopk = 64;    // choices of a token (one lane each)
 constexpr uint32_t kRouteTokens = 64;     // tokens per routing workgroup (one bit each of a 64-bit mask)
 

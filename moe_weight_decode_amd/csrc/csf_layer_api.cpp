@@ -203,7 +203,7 @@ csf_status gated_stack(const csf_stack *s, bool need_streams, int64_t &K) {
         int64_t(s->rows) * s->cols >= (int64_t(1) << 24))
         return CSF_E_SHAPE;
     K = (mx ? 32 : 16) * int64_t(s->cols);
-    if (K % 32 != 0 || K > 8192) return CSF_E_SHAPE;
+    if (K % 32 != 0 || K > int64_t(csf::kGatedMaxK)) return CSF_E_SHAPE;
     if (!need_streams) return CSF_OK;
     if (s->bases == nullptr || s->offsets == nullptr || s->exc_prefix == nullptr || s->tile_index == nullptr)
         return CSF_E_NULL;
