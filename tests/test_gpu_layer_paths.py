@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import workloads
-from test_gpu_layer import U, Gated, check_gated, f64, near, normal
+from oracle import layer as ref
+from test_gpu_layer import HALF, TINY, U, Gated, check_gated, f64, near, normal
 
 csf = pytest.importorskip("moe_weight_decode_amd")
 
@@ -93,6 +94,149 @@ def test_gated_backward_writes_routed_slots_only(dev):
         dx.data_ptr(), dgu.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
     for got, full in ((dx, want[0]), (dgu, want[1])):
         assert (got[:first] == 7).all() and torch.equal(got[first:], full[first:])
+
+
+KINDS = {"nvfp4": (workloads.NVFP4, False), "mxfp4": (workloads.MXFP4, False), "mx8": (workloads.MXFP4, True)}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("E,F,K,counts", [
+    (3, 24, 5120, [1, 0, 17]), (2, 20, 8192, [2, 19]), (2, 17, 4128, [1, 1]),  # more than 4 chunks of K a wave
+    (40, 24, 64, [15] * 40),                                                   # more slots than come with the routing
+    (300, 9, 96, [0, 1, 2] * 100),
+    (9, 33, 1056, [0, 40, 0, 1, 0, 90, 3, 0, 16]),                             # few slots over all, many of one expert
+])
+def test_gated_few_slots(dev, E, F, K, counts, kind):
+    assert sum(counts) < 20 * E
+    fmt, x8 = KINDS[kind]
+    c = Gated(E, F, K, counts, fmt, x8, seed=E + F + K)
+    h, gu = c.forward(save=True)
+    check_gated(c, h, gu)
+    assert torch.equal(c.forward(), h)
+    h2, gu2 = c.forward(save=True, dense_scales=c.dense())
+    assert torch.equal(h2, h) and torch.equal(gu2, gu)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_few_slots_with_nan_tokens(dev, kind):
+    fmt, x8 = KINDS[kind]
+    c = Gated(3, 40, 160, [5, 0, 30], fmt, x8, seed=9, T=12)
+    clean = c.forward()
+    c.x[3] = 0x7f if x8 else float("nan")
+    h = c.forward()
+    hit = torch.from_numpy(c.rows == 3).to(dev)
+    assert hit.any() and h[hit].isnan().all() and torch.equal(h[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_without_their_counters(dev, kind):
+    # scales decoded beforehand and no workspace: the tiles are dealt out in turn
+    fmt, x8 = KINDS[kind]
+    c = Gated(5, 300, 96, [1, 0, 700, 16, 300], fmt, x8, seed=31)
+    h, gu = c.forward(save=True)
+    check_gated(c, h, gu)
+    d, dense, S = c.stack.descriptor(), c.dense(), len(c.rows)
+    out, ogu = torch.empty_like(h), torch.empty_like(gu)
+    assert csf.library().csf_moe_gated(
+        ctypes.byref(d), dense.data_ptr(), c.tw.data_ptr(), c.x.data_ptr(), c.xs.data_ptr() if x8 else None, c.x.shape[0],
+        c.ta.data_ptr(), c.te.data_ptr(), c.tr.data_ptr(), S, out.data_ptr(), ogu.data_ptr(), None, 0,
+        torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(out, h) and torch.equal(ogu, gu)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_activations_past_31_bit_offsets(dev, kind):
+    # more activations than a tile's offsets reach: many slots, taken as few are
+    fmt, x8 = KINDS[kind]
+    c = Gated(2, 40, 32, [70, 90], fmt, x8, seed=33, T=100)
+    T = (2 ** 31 // 32 if x8 else 2 ** 31 // 64) + 1000
+    rng = np.random.default_rng(5)
+    at = torch.from_numpy(np.sort(rng.choice(T - 1, 99, replace=False)).astype(np.int32)).to(dev)
+    at = torch.cat((at, torch.tensor([T - 1], dtype=torch.int32, device=dev)))
+    x = torch.zeros(T, 32, dtype=c.x.dtype, device=dev)
+    x[at.long()] = c.x
+    if x8:
+        xs = torch.zeros(T, 1, dtype=torch.uint8, device=dev)
+        xs[at.long()] = c.xs
+        c.xs = xs
+    c.x, c.tr = x, at[c.tr.long()]
+    h, gu = c.forward(save=True)
+    check_gated(c, h, gu)
+
+
+# ------------------------------------------------------------------ many tokens
+
+def route_of_many(logits, k, renorm):
+    """oracle.layer.route for many tokens at once."""
+    l = np.where(np.isnan(logits), -np.inf, logits)
+    T, E = l.shape
+    order = np.argsort(-l, axis=1, kind="stable")[:, :k]
+    top = np.take_along_axis(l, order, 1)
+    on = top > -np.inf
+    experts = np.where(on, order, -1)
+    most = np.where(on[:, :1], top[:, :1], 0.0)
+    p = np.where(on, np.exp(top - most), 0.0)
+    whole = p.sum(1, keepdims=True) if renorm else np.exp(l - most).sum(1, keepdims=True)
+    gates = np.where(on, p / np.where(on[:, :1], whole, 1.0), 0.0)
+    flat = np.where(experts < 0, E, experts).reshape(-1)
+    by = np.argsort(flat, kind="stable")
+    start = np.searchsorted(flat[by], np.arange(E + 1))
+    rows, slots = np.full(T * k, -1), np.full(T * k, -1)
+    rows[:start[E]] = by[:start[E]] // k
+    slots[by[:start[E]]] = np.arange(start[E])
+    return experts, gates, start, rows, slots.reshape(T, k)
+
+
+def same_routing(r, want, k, E, renorm):
+    e, g, start, rows, slots = want
+    assert np.array_equal(r.experts.cpu().numpy(), e) and np.array_equal(r.expert_start.cpu().numpy(), start)
+    assert np.array_equal(r.rows.cpu().numpy(), rows) and np.array_equal(r.slots.cpu().numpy(), slots)
+    near(r.gates, g, ((k if renorm else E) + 24) * U * g, "gates")
+
+
+def test_the_oracle_of_many_is_the_oracle(dev):
+    rng = np.random.default_rng(1)
+    l = rng.integers(-3, 3, (90, 11)).astype(np.float64)  # many equal ones
+    l[rng.random(l.shape) < 0.3] = -np.inf
+    l[7], l[8, 3] = -np.inf, np.nan
+    for renorm in (True, False):
+        for a, b in zip(route_of_many(l, 4, renorm), ref.route(l, 4, renorm)):
+            assert np.allclose(a, b, rtol=1e-14, atol=0)
+
+
+# 16 lanes a token from 2048 tokens on (2, 4, 8, 16, 24 or 32 logits a lane), 64 above 512 experts or 16 choices;
+# workgroups' counts added up by each up to 16384 tokens, by a kernel of their own beyond
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,E,k", [(2048, 33, 3), (2049, 2, 2), (2049, 65, 16), (2047, 100, 4), (2111, 256, 8), (4100, 384, 8),
+                                   (2100, 512, 16), (2050, 513, 3), (2060, 64, 17), (2048, 16, 1), (16384, 40, 2),
+                                   (16385, 40, 2), (20000, 7, 3), (17000, 600, 2)])
+def test_route_of_many_tokens(dev, T, E, k, dtype):
+    rng = np.random.default_rng(T + 31 * E + k)
+    logits = normal(rng, T, E, dtype=dtype, scale=1.5)
+    masked = logits.masked_fill(torch.from_numpy(rng.random((T, E)) < 0.3).to(dev), float("-inf"))
+    masked[T // 2] = float("-inf")
+    masked[T - 1, 1:] = float("nan")
+    for renorm in (True, False):
+        for l in (logits, masked):
+            want = route_of_many(f64(l.float()), k, renorm)
+            same_routing(csf.route(l, k, renorm=renorm), want, k, E, renorm)
+    equal = torch.zeros(T, E, dtype=dtype, device=dev)
+    equal[:, ::2] = -0.0
+    assert torch.equal(csf.route(equal, k).experts, torch.arange(k, dtype=torch.int32, device=dev).expand(T, k))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(9000, 24), (4100, 1000), (3100, 1030), (1100, 8200), (1030, 20000)])
+def test_norm_backward_of_many_tokens(dev, T, D, dtype):
+    # several rows to a workgroup, its two buffers of partial sums in turn
+    rng = np.random.default_rng(T + D)
+    total, dy, ds = (normal(rng, T, D, dtype=dtype) for _ in range(3))
+    w = 1.0 + normal(rng, D, scale=0.1)
+    rstd = csf.rms_norm(total, w).rstd
+    dx, dw = csf.rms_norm_backward(dy, total, w, rstd, dsum=ds)
+    wx, ww, mx, mw = ref.rms_norm_backward(f64(dy), f64(total), f64(w), f64(rstd), f64(ds))
+    near(dx, wx, HALF[dtype] * np.abs(wx) + (D + 16) * U * mx * (1 + HALF[dtype]) + TINY[dtype], "dx")
+    near(dw, ww, (T + 16) * U * mw, "dweight")
 
 
 # ------------------------------------------------------------------ launches past 2^32 threads
