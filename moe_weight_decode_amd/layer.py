@@ -57,7 +57,7 @@ def declare(lib):
 class Normed(NamedTuple):
     """Result of ``rms_norm``."""
     out: torch.Tensor                  # [T, D]: the inputs' type, or E4M3 codes (uint8)
-    sum: torch.Tensor                  # [T, D]: x + residual
+    sum: torch.Tensor                  # [T, D]: x + residual (without a residual x itself, not a copy)
     rstd: torch.Tensor                 # float32 [T]
     scales: torch.Tensor | None        # uint8 [T, ceil(D / 32)] (E8M0) with mxfp8
 
