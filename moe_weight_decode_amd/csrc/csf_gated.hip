@@ -915,6 +915,9 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_dx_kernel(GatedBac
     const uint32_t mtiles = tile_prefix(a.expert_start, a.E, a.S, s_prefix, s_scan);
     const uint32_t ktiles = (K + kDxCols - 1u) / kDxCols, total = mtiles * ktiles;
     const uint32_t steps = (N + kDxRows - 1u) / kDxRows;
+    // An offset past every tile's range of dgu: a constant would not be, since 128 slots of up to 2^24 - 2 rows reach
+    // 2^32 - 512 bytes.
+    const uint32_t past = kTileTokens * N * 2u;
 
     uint32_t u = blockIdx.x, ustep = gridDim.x, uend = total;
     if ((gridDim.x & (kXcds - 1u)) == 0) {
@@ -928,10 +931,7 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_dx_kernel(GatedBac
         const Tile at = find_tile(s_prefix, a.expert_start, a.E, a.S, mt);
         const uint32_t e = at.e, t0 = at.t0, count = at.count;
         const float alpha = a.alpha[e];
-        // Slots past the tile's and rows past 2F read 0: the range's own end is past it at every offset.  A constant would
-        // not be, since 128 slots of up to 2^24 - 2 rows reach 2^32 - 512 bytes.
-        const uint32_t past = count * N * 2u;
-        const rsrc_t rd = make_rsrc(a.dgu + (uint64_t)t0 * N, past);
+        const rsrc_t rd = make_rsrc(a.dgu + (uint64_t)t0 * N, count * N * 2u);  // slots past the tile's read 0
         const rsrc_t rw = make_rsrc(a.w + (uint64_t)e * N * (K / 2u), N * (K / 2u));
         const uint8_t *scales = a.dense + (uint64_t)e * N * C;
         const bool some = k0 + kDxWave * wave < K;  // the wave has columns
