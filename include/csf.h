@@ -453,6 +453,9 @@ csf_status csf_route_backward(int32_t dtype, const float *dgates, const void *lo
  * No factor is rounded, and products are summed in float32 (MXFP4 weights with
  * scale bytes 0, 1, 253 or 254 and bfloat16 x follow the hardware's conversion);
  * h is computed from the unrounded g and u.
+ * Two kernels: from 20 slots per expert on (num_slots, however they spread) and
+ *   with x of less than 2^31 bytes, tiles of many slots; else units of few,
+ *   which take an expert's weights again for every 16 of its slots.
  * workspace: with 20 or more slots per expert its first 64 bytes deal out the
  *   kernel's tiles and the rest holds decoded scales; with dense_scales it may be
  *   NULL or just those 64 bytes (without them the tiles are dealt out in turn,

@@ -363,17 +363,22 @@ __global__ __launch_bounds__(kUnitThreads, NCH > 4 ? 2 : 4) void csf_gated_unit_
 // ahead of the kernel): a tile would spend three dependent round trips on
 // expanding its own.
 //
-// bfloat16 activations: widening an E4M3-scaled weight takes two vector
-// instructions (a lane's weights of a 16 x 16 x 32 product 16), so that at
-// 128 slots there are two of them to a matrix instruction, at 96 three; the
-// matrix cores are busy 31 % of the time, the rest is vector issue, the tiles'
-// ends and columns that fill no tile (800 of 896).  131,072 slots through 512
-// experts, K = 2048, 2 x 800 rows: 1.18 to 1.21 ms, 720 TFLOP/s.
+// 131,072 slots through 512 experts, K = 2048, 2 x 800 rows, NVFP4, bfloat16
+// activations: 1.15 to 1.21 ms, 720 to 750 TFLOP/s.  Of that the matrix cores
+// are busy 0.38 ms and vector instructions, most of them widening (two to a
+// weight, two to three to a matrix instruction), issue for 0.35 ms; the two
+// waves of a SIMD spend a third of their time issuing, a third waiting for the
+// other's instructions and a third for loads, LDS and barriers.  Neither bounds
+// it alone: what does not overlap is a tile's first loads and its stores, and
+// the last of seven column tiles, in which one wave of four has columns (800 of
+// 896).  35 to 53 vector registers are spilled in a tile's beginning and end and
+// between steps, none among the products.
 // 8-bit activations need no widening, but two products for their two classes:
-// 0.31 ms of the matrix cores' time, 0.19 ms of vector issue for the masks and
-// the loads' path through the L2s overlap in part.  65,536 slots through 384
-// experts, K = 5120, 2 x 512 rows: 0.80 ms, 860 TFLOP/s (in one class, with
-// sums cut as said above, 0.58 ms).
+// 65,536 slots through 384 experts, K = 5120, 2 x 512 rows, MXFP4: 0.80 to 0.84
+// ms, 840 TFLOP/s (in one class, with sums cut as said above, 0.58 ms).  The
+// matrix cores are busy 0.31 ms, vector instructions issue for 0.28 ms, and the
+// loads take 3.7 GB through the L2s; waits are shared as above.  The same with
+// bfloat16 activations takes 0.79 ms.
 
 constexpr uint32_t kTileTokens = 128;
 constexpr uint32_t kTileCols = 128;
@@ -890,9 +895,11 @@ __global__ __launch_bounds__(kGatedThreads) void csf_gated_dgu_kernel(GatedBackw
 // to bfloat16, the form it is returned in: half a step of 2^-8 on each factor,
 // as the result's own rounding, for matrix cores that take 16 bits.
 //
-// Two vector instructions per widened weight, as in the forward kernel, bound
-// it: 131,072 slots, K = 2048, 2 x 800 rows in 1.31 ms with the decode and the
-// pass over dgu (0.2 ms, bound by memory), 655 TFLOP/s.
+// 131,072 slots, K = 2048, 2 x 800 rows, NVFP4 in 1.29 to 1.31 ms, 660 TFLOP/s:
+// the decode 0.05 ms, the pass over dgu 0.2 ms (bound by memory), then the
+// products 1.05 ms, of which the matrix cores are busy 0.38 and vector
+// instructions issue for 0.32; a third of the waves' time are waits for loads,
+// LDS and barriers.
 constexpr uint32_t kDxCols = 256;   // columns of dx per tile
 constexpr uint32_t kDxWave = 64;    // per wave
 constexpr uint32_t kDxRows = 64;    // weight rows per step
@@ -1134,10 +1141,12 @@ __global__ __launch_bounds__(kGatedThreads, 2) void csf_gated_dx_kernel(GatedBac
 }  // namespace
 
 // Units take every expert's weights once per 16 slots, tiles once per 128, after a decode of the scales: 64 experts,
-// K = 2048, 2 x 800 rows, with 16, 32 and 64 slots each 79, 116 and 198 us by units, 90, 92 and 103 us by tiles.
+// K = 2048, 2 x 800 rows, with 16, 32 and 64 slots each 79, 116 and 198 us by units, 90, 92 and 103 us by tiles.  The
+// host knows the slots' number, not how they spread: 6000 slots of 384 experts take 340 us by units and 313 by tiles
+// where all have as many, 198 and 97 us where 8 experts have them all.
 bool gated_by_tiles(uint32_t E, uint32_t S) { return S >= 20u * E; }
 
-// 31-bit buffer offsets reach the activations.
+// 31-bit buffer offsets reach the activations; units take more of them.
 bool tiles_reach(uint32_t T, uint32_t K, bool x8) { return uint64_t(T) * K * (x8 ? 1u : 2u) < (uint64_t(1) << 31); }
 
 hipError_t launch_gated_tiles(const GatedArgs &a, hipStream_t stream) {

@@ -19,8 +19,8 @@
 //
 // A row is taken by one wave up to 1024 columns and by a workgroup above, since
 // a wave's 64 lanes would need more registers than hide the loads' latency.
-// Measured: 16384 x 5120 bfloat16 122 us, 5.5 TB/s (a large copy's rate); 512 x
-// 5120 with 8 experts' outputs combined and 8-bit output 17.3 us, 5.5 TB/s; one
+// Measured: 16384 x 5120 bfloat16 123 us, 5.4 TB/s (a large copy's rate); 512 x
+// 5120 with 8 experts' outputs combined and 8-bit output 17.0 to 17.5 us, 5.6 TB/s; one
 // row of 2048 4.1 us, a launch and two round trips.
 #include "csf_layer_device.h"
 
@@ -157,7 +157,11 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void csf_norm_kernel
 // registers (a thread's columns are the same for every row); the shares are
 // added in the groups' order by a second kernel, so the result does not
 // depend on timing.  Bound by memory and, in short calls, by the second launch:
-// 8191 x 2048 bfloat16 31.5 us, 4.3 TB/s.
+// 8191 x 2048 bfloat16 30.2 to 31.1 us, 4.4 TB/s.  Slower for what it moves are
+// up to 1024 rows above 1024 columns, each a group with a row of partial sums of
+// its own (1024 x 5120 22.8 us, 1.8 TB/s), and more than 8192 columns: 1024
+// threads leave 128 registers each, and 275 to 309 are spilled (4096 x 16384
+// 705 us, 0.8 TB/s).
 template <typename T, uint32_t CHUNKS, uint32_t THREADS>
 __global__ __launch_bounds__(THREADS) void csf_norm_backward_kernel(NormBackwardArgs a) {
     __shared__ float lds[2][THREADS / kWave];

@@ -32,8 +32,9 @@ namespace csf {
 namespace {
 
 constexpr uint32_t kRouteThreads = 1024;
-// Counts of so many workgroups are added up in 16 bits, all in flight at once.  A kernel of its own for the offsets
-// costs more up to there (8192 x 384: 39.5 against 34.8 us, 16384: 52.9 against 52.3, calls from Python).
+// Counts of so many workgroups are added up in 16 bits, all in flight at once: four loads of 16 bytes a lane (the bits
+// would do for 1023 workgroups).  A kernel of its own for the offsets costs more up to there (8192 x 384: 39.5 against
+// 34.8 us, 16384: 52.9 against 52.3, calls from Python); beyond, where every workgroup reads all counts, it was not tried.
 constexpr uint32_t kRouteSumGroups = 256;
 
 __device__ __forceinline__ uint32_t order_key(float v) {
