@@ -372,9 +372,9 @@ __global__ __launch_bounds__(kUnitThreads, NCH > 4 ? 2 : 4) void csf_gated_unit_
 // it alone: what does not overlap is a tile's first loads and its stores, and
 // the last of seven column tiles, in which one wave of four has columns (800 of
 // 896).  35 to 53 vector registers are spilled in a tile's beginning and end and
-// between steps, none among the products.
+// between steps; one load of them a step lies among the products (8 bits).
 // 8-bit activations need no widening, but two products for their two classes:
-// 65,536 slots through 384 experts, K = 5120, 2 x 512 rows, MXFP4: 0.80 to 0.84
+// 65,536 slots through 384 experts, K = 5120, 2 x 512 rows, MXFP4: 0.80 to 0.85
 // ms, 840 TFLOP/s (in one class, with sums cut as said above, 0.58 ms).  The
 // matrix cores are busy 0.31 ms, vector instructions issue for 0.28 ms, and the
 // loads take 3.7 GB through the L2s; waits are shared as above.  The same with
@@ -895,7 +895,7 @@ __global__ __launch_bounds__(kGatedThreads) void csf_gated_dgu_kernel(GatedBackw
 // to bfloat16, the form it is returned in: half a step of 2^-8 on each factor,
 // as the result's own rounding, for matrix cores that take 16 bits.
 //
-// 131,072 slots, K = 2048, 2 x 800 rows, NVFP4 in 1.29 to 1.31 ms, 660 TFLOP/s:
+// 131,072 slots, K = 2048, 2 x 800 rows, NVFP4 in 1.29 to 1.33 ms, 655 TFLOP/s:
 // the decode 0.05 ms, the pass over dgu 0.2 ms (bound by memory), then the
 // products 1.05 ms, of which the matrix cores are busy 0.38 and vector
 // instructions issue for 0.32; a third of the waves' time are waits for loads,

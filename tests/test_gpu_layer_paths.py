@@ -451,3 +451,25 @@ def test_bound_calls_captured_later_and_on_another_stream(dev):
         out = [call() for call in calls]
         torch.cuda.current_stream().wait_stream(side)
         same(out, plain())
+
+
+def test_calls_on_the_default_stream_from_another(dev):
+    """The default stream is no stream made here: it has no handle of its own."""
+    rng = np.random.default_rng(29)
+    x, w = normal(rng, 700, 2048, dtype=torch.bfloat16), torch.ones(2048, device=dev)
+    want = csf.rms_norm(x, w, x)
+    torch.cuda.synchronize()
+    side, main = torch.cuda.Stream(), torch.cuda.default_stream()
+    big = torch.empty(64 << 20, dtype=torch.float32, device=dev)
+    with torch.cuda.stream(side):
+        y = torch.zeros_like(x)
+        call = csf.bound(csf.rms_norm, y, w, y)
+        for i in range(10):
+            big.fill_(float(i))
+        y.copy_(x)
+        got = csf.rms_norm(y, w, y, stream=main)  # waits for the copy
+    assert torch.equal(got.out, want.out) and torch.equal(got.sum, want.sum)
+    torch.cuda.synchronize()
+    out = call().out  # bound under the side stream, called on the default one
+    del call
+    assert torch.equal(out, want.out)
