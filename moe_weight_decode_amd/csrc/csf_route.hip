@@ -405,12 +405,13 @@ __global__ __launch_bounds__(256) void csf_route_backward_kernel(RouteBackwardAr
         most = key_value(top);  // of no use where every logit is masked
 #pragma unroll
         for (uint32_t i = 0; i < EPL; ++i) {
-            v[i] = v[i] > -__builtin_inff() ? expf(v[i] - most) : 0.f;
-            sum += v[i];
+            v[i] = v[i] > -__builtin_inff() ? expf(v[i] - most) : -1.f;  // below 0: masked
+            sum += fmaxf(v[i], 0.f);
         }
         const float scale = top == 0u ? 0.f : mean / wave_sum(sum);
+        // a masked logit gets 0, not 0 times a mean that may be infinite or NaN
 #pragma unroll
-        for (uint32_t i = 0; i < EPL; ++i) out[i] = fmaf(-v[i], scale, out[i]);
+        for (uint32_t i = 0; i < EPL; ++i) out[i] = v[i] < 0.f ? out[i] : fmaf(-v[i], scale, out[i]);
     }
     T *dst = static_cast<T *>(a.dlogits) + row + first;
     if constexpr (EPL % 8u == 0) {

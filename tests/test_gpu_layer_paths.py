@@ -225,6 +225,25 @@ def test_route_of_many_tokens(dev, T, E, k, dtype):
     assert torch.equal(csf.route(equal, k).experts, torch.arange(k, dtype=torch.int32, device=dev).expand(T, k))
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_masked_logits_get_no_gradient_whatever_the_gates_get(dev, value, renorm):
+    rng = np.random.default_rng(41)
+    T, E, k = 9, 130, 4
+    logits = normal(rng, T, E).masked_fill(torch.from_numpy(rng.random((T, E)) < 0.4).to(dev), float("-inf"))
+    logits[7] = float("nan")
+    r = csf.route(logits, k, renorm=renorm)
+    dg = normal(rng, T, k)
+    clean = csf.route_backward(dg, logits, r.experts, r.gates, renorm=renorm)
+    dg[3, 1] = value
+    dg[7] = value  # of no choice
+    got = csf.route_backward(dg, logits, r.experts, r.gates, renorm=renorm)
+    masked = ~(logits > float("-inf"))
+    assert (got[masked] == 0).all()
+    others = torch.arange(T, device=dev) != 3
+    assert torch.equal(got[others], clean[others]) and not got[3].isfinite().all()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("T,D", [(9000, 24), (4100, 1000), (3100, 1030), (1100, 8200), (1030, 20000)])
 def test_norm_backward_of_many_tokens(dev, T, D, dtype):
