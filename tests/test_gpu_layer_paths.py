@@ -9,7 +9,7 @@ import torch
 
 import workloads
 from oracle import layer as ref
-from test_gpu_layer import HALF, TINY, U, Gated, check_gated, f64, near, normal
+from test_gpu_layer import HALF, TINY, U, Gated, check_gated, f64, near, normal, shifted
 
 csf = pytest.importorskip("moe_weight_decode_amd")
 
@@ -142,6 +142,31 @@ def test_tiles_without_their_counters(dev, kind):
         c.ta.data_ptr(), c.te.data_ptr(), c.tr.data_ptr(), S, out.data_ptr(), ogu.data_ptr(), None, 0,
         torch.cuda.current_stream().cuda_stream) == 0
     assert torch.equal(out, h) and torch.equal(ogu, gu)
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 8], [70, 0, 130]])
+@pytest.mark.parametrize("F", [40, 41])
+def test_gated_tensors_at_their_least_alignment(dev, F, counts):
+    c = Gated(3, F, 96, counts, workloads.NVFP4, seed=35)
+    S, lib, stream = len(c.rows), csf.library(), torch.cuda.current_stream().cuda_stream
+    h, gu = c.forward(save=True)
+    dh = normal(np.random.default_rng(2), S, F, dtype=torch.bfloat16)
+    dx, dgu = csf.moe_gated_backward(c.stack, c.dense(), c.tw, dh, gu, c.ta, c.te)
+    d, alpha, es, rows = c.stack.descriptor(), shifted(c.ta, 1), shifted(c.te, 1), shifted(c.tr, 1)
+    need = lib.csf_moe_gated_workspace(ctypes.byref(d), S)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    out, ogu, odgu = shifted(torch.zeros_like(h), 1), shifted(torch.zeros_like(gu), 1), shifted(torch.zeros_like(dgu), 2)
+    odx, dense = torch.zeros_like(dx), shifted(c.dense(), 1)
+    assert lib.csf_moe_gated(ctypes.byref(d), None, c.tw.data_ptr(), c.x.data_ptr(), None, c.x.shape[0], alpha.data_ptr(),
+                             es.data_ptr(), rows.data_ptr(), S, out.data_ptr(), ogu.data_ptr(), ws.data_ptr(), need, stream) == 0
+    assert torch.equal(out, h) and torch.equal(ogu, gu)
+    assert lib.csf_moe_gated(ctypes.byref(d), dense.data_ptr(), c.tw.data_ptr(), c.x.data_ptr(), None, c.x.shape[0],
+                             alpha.data_ptr(), es.data_ptr(), rows.data_ptr(), S, out.data_ptr(), ogu.data_ptr(), None, 0, stream) == 0
+    assert torch.equal(out, h) and torch.equal(ogu, gu)
+    dh, gu = shifted(dh, 1), shifted(gu, 1)
+    assert lib.csf_moe_gated_backward(ctypes.byref(d), dense.data_ptr(), c.tw.data_ptr(), dh.data_ptr(), gu.data_ptr(), S,
+                                      alpha.data_ptr(), es.data_ptr(), odx.data_ptr(), odgu.data_ptr(), stream) == 0
+    assert torch.equal(odx, dx) and torch.equal(odgu, dgu)
 
 
 @pytest.mark.parametrize("kind", KINDS)
